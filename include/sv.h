@@ -85,8 +85,9 @@ typedef enum sv_weight_mode { SV_W_RAW = 0, SV_W_GROUP_NORM = 1 } sv_weight_mode
 #define SV_DEV_NO_FINITE 0x2      /* a logit row with no finite value */
 #define SV_DEV_TIMEOUT 0x4        /* a bounded wait for a bulk copy gave up */
 #define SV_DEV_BAD_TREE 0x8       /* parents[] is not a tree in BFS order, or depth > max_depth */
-#define SV_DEV_BAD_INDEX 0x10     /* a top-K index outside [0, V) given to sv_kd_kl_loss */
-#define SV_DEV_BAD_LEN 0x20       /* a draft_len outside [0, k] given to sv_verify_chain_ragged */
+#define SV_DEV_BAD_INDEX 0x10     /* a top-K index outside [0, V), or a page or slot outside the cache */
+#define SV_DEV_BAD_LEN 0x20       /* a draft_len outside [0, k], or a cache length out of range */
+#define SV_DEV_NO_PAGES 0x40      /* sv_kv_plan ran out of free pages */
 #define SV_DEV_ERROR_MASK 0xff
 #define SV_DEV_RESIDUAL_ZERO 0x100 /* info: a rejection met zero residual mass; the target row was sampled */
 #define SV_DEV_TOPK_SLOW 0x200     /* info: massive ties sent a top-K through the slow exact path */
@@ -372,6 +373,151 @@ SV_API sv_status sv_kd_grad(const float* topk_logp, const int32_t* topk_idx, int
                             void* stream);
 
 /*
+ * The paged key-value cache of a verification step.  The pages' engines keep
+ * one (ReSpec notes, section 3: a request that switches between plain and
+ * speculative decoding fills the cache for the tokens it lacks); no page
+ * gives its layout, so the layout below is this library's.
+ *
+ * Keys and values of a layer live in a pool of `num_pages` pages of
+ * `page_size` tokens.  Request b's token at position t is at offset
+ * t % page_size of page block_table[b, t / page_size].  A step writes
+ * new_len[b] new tokens (the last emitted token and its drafts, a candidate
+ * tree, or a prompt) behind the kv_len[b] committed ones, attends from them,
+ * and after verification the next plan commits the accepted ones:
+ *
+ *   sv_kv_plan -> (projections) -> sv_kv_append -> sv_kv_attend -> (logits)
+ *     -> sv_verify_chain_ragged or sv_verify_tree_* -> [sv_kv_commit] -> sv_kv_plan ...
+ *
+ * Pages of different requests, and of one request's table, are distinct
+ * wherever a call writes; sv_kv_attend also reads shared ones.
+ */
+typedef struct sv_kv_cache {
+  void* k;              /* keys; element (page, token, head, i) at page * page_stride +      */
+  void* v;              /* values        token * token_stride + head * head_stride + i       */
+  sv_dtype dtype;
+  int num_pages, page_size;
+  int heads, head_dim;  /* key heads; 1 <= head_dim <= 256 */
+  int64_t page_stride, token_stride, head_stride; /* elements; tokens must not overlap */
+} sv_kv_cache;
+
+/*
+ * sv_kv_plan -- block tables and slots of the next step, from the lengths.
+ *
+ * Operation, for requests b in order:
+ *   commit_b: of the written[b] tokens that the last step wrote,
+ *     accepted_len[b] + 1 stay (the root and the accepted drafts);
+ *     all of them without accepted_len; none if written[b] == 0 (or written
+ *     is NULL) or accepted_len[b] < 0.
+ *   L_b = kv_len[b] + commit_b, or 0 if release[b] != 0 (the request ended).
+ *   N_b = ceil((L_b + new_len[b]) / page_size) pages (new_len counts as 0
+ *     for a released request).
+ *   A request that holds more than N_b pages gives the surplus back: its
+ *   pages N_b, N_b + 1, ... are pushed on the free stack.  After all of those
+ *   the others take the pages they lack from the top of the stack.  Requests
+ *   are served in order until one finds too few pages; it and every later
+ *   request that lacks pages get none and no new tokens this step
+ *   (q_len[b] = 0, SV_DEV_NO_PAGES); their commit stands.
+ *   slot_map[b, i] = block_table[b, t / page_size] * page_size + t % page_size
+ *   with t = L_b + i for i < q_len[b], else -1; positions[b, i] = t, else -1.
+ *
+ * Arguments
+ *   kv_len [B]; written, accepted_len, release [B] or NULL; new_len [B] in
+ *   [0, max_new]; pages [B] (pages held); free_count [1]; free_pages
+ *   [num_pages]: a stack, its bottom at index 0.  All int32.
+ *   block_table [B, max_pages] int32, in and out: only entries a request gains are
+ *   written, and entries past a request's pages keep what they held.
+ *   kv_len_out, pages_out, q_len [B], free_count_out [1]: out; each may be
+ *   the array of an input.  slot_map [B, max_new] int64, positions
+ *   [B, max_new] int32 (or NULL): out.
+ *   0 <= B <= 8192, B * max_pages < 2^31, B * max_new < 2^31.
+ *   A request with a length out of range (L_b + new_len[b] beyond max_pages
+ *   pages, accepted_len[b] >= written[b] > 0, committed tokens without a page, ...)
+ *   is left as it is, gets no new tokens and sets SV_DEV_BAD_LEN.  A page id
+ *   outside [0, num_pages) sets SV_DEV_BAD_INDEX; its tokens' slots are -1.
+ *   No workspace.
+ */
+SV_API sv_status sv_kv_plan(const int32_t* kv_len, const int32_t* written,
+                            const int32_t* accepted_len, const int32_t* release,
+                            const int32_t* new_len, int B, int max_new, int page_size,
+                            int num_pages, int32_t* block_table, int max_pages,
+                            const int32_t* pages, int32_t* free_pages, const int32_t* free_count,
+                            int32_t* kv_len_out, int32_t* pages_out, int32_t* free_count_out,
+                            int32_t* q_len, int64_t* slot_map, int32_t* positions,
+                            int32_t* device_status, void* stream);
+
+/*
+ * sv_kv_append -- writes new tokens' keys and values to their slots.
+ *   k, v [B, n, heads, head_dim] of the cache's type; the rows of a token are
+ *   dense, tokens token_stride and requests batch_stride elements apart (so
+ *   they may be parts of a fused projection's output).
+ *   slot_map [B, n] int64: tokens with a negative slot are skipped; a slot
+ *   >= num_pages * page_size is skipped and sets SV_DEV_BAD_INDEX.  Slots
+ *   must be distinct (those of sv_kv_plan are): of two tokens with one slot
+ *   either may remain, or a mixture.
+ */
+SV_API sv_status sv_kv_append(const sv_kv_cache* cache, const void* k, const void* v, int B, int n,
+                              int64_t batch_stride, int64_t token_stride, const int64_t* slot_map,
+                              int32_t* device_status, void* stream);
+
+/*
+ * sv_kv_attend -- attention of the new tokens over the cache.
+ *
+ * Operation: token i < q_len[b] of request b attends to the kv_len[b]
+ *   committed tokens, to itself and to its ancestors among the new tokens,
+ *   whose keys and values are in the cache at positions kv_len[b] + j.
+ *   parents == NULL: a chain, the ancestors are the tokens before it.
+ *   Otherwise parents[b, i] is its parent (-1: none, else < i).
+ *   Query head x reads key head x / (q_heads / heads).
+ *   out[b, i, x] = sum_j softmax_j(scale * q[b, i, x] . k_j) v_j,
+ *   lse[b, i, x] = log sum_j exp(scale * q[b, i, x] . k_j).
+ *   A key that a row does not attend to never affects it, whatever the cache
+ *   holds there.  Tokens i >= q_len[b] give zeros and lse -inf.
+ *
+ * Arguments
+ *   q [B, n, q_heads, head_dim] of the cache's type, the heads of a token
+ *   dense, strides in elements as in sv_kv_append.  out [B, n, q_heads,
+ *   head_dim] dense, of the cache's type; lse [B, n, q_heads] fp32 or NULL.
+ *   block_table [B, max_pages], kv_len [B]; q_len [B] or NULL (n everywhere);
+ *   parents [B, n] or NULL: int32.
+ *   1 <= n <= 1024, q_heads a multiple of heads, scale finite.
+ *   A request with lengths out of range sets SV_DEV_BAD_LEN, a row whose keys
+ *   are on a page outside [0, num_pages) SV_DEV_BAD_INDEX, a row with a bad
+ *   parent on its way up SV_DEV_BAD_TREE; their outputs are NaN (with
+ *   BAD_TREE and BAD_INDEX, rows of the same request that share a tile may be NaN too).
+ *   workspace: sv_kv_attend_workspace_size(...) bytes.
+ * Sums and softmax statistics are fp32.  The split of a sequence over the
+ * device's blocks depends on all lengths of the batch, so a request's last
+ * bits can differ between batches; a repeated call gives the same bits.
+ */
+SV_API size_t sv_kv_attend_workspace_size(int B, int n, int q_heads, int heads, int head_dim,
+                                          sv_dtype dtype);
+SV_API sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_stride,
+                              int64_t token_stride, int B, int n, int q_heads,
+                              const int32_t* block_table, int max_pages, const int32_t* kv_len,
+                              const int32_t* q_len, const int32_t* parents, float scale, void* out,
+                              float* lse, void* workspace, size_t workspace_bytes,
+                              int32_t* device_status, void* stream);
+
+/*
+ * sv_kv_commit -- after a tree was verified, moves the accepted path to the
+ * front of the step's tokens: position kv_len[b] + i takes the key and value
+ * of position kv_len[b] + accepted_nodes[b, i], i = 0..accepted_len[b], in
+ * each of `layers` caches that lie layer_stride elements apart from `cache`.
+ * The next sv_kv_plan then commits accepted_len[b] + 1 tokens.
+ *   accepted_nodes [B, width] and accepted_len [B] as sv_verify_tree_* give
+ *   them (width = max_depth + 1 <= 1024; the path ascends from node 0; entries
+ *   past the path are not read; accepted_len -1 or 0 moves nothing).
+ *   A path that does not ascend from 0 sets SV_DEV_BAD_TREE, a position
+ *   outside the table or accepted_len >= width SV_DEV_BAD_LEN, a bad page
+ *   SV_DEV_BAD_INDEX; such a request's cache is left as it is.
+ *   0 <= B <= 65535.  No workspace.
+ */
+SV_API sv_status sv_kv_commit(const sv_kv_cache* cache, int layers, int64_t layer_stride, int B,
+                              const int32_t* block_table, int max_pages, const int32_t* kv_len,
+                              const int32_t* accepted_nodes, int width,
+                              const int32_t* accepted_len, int32_t* device_status, void* stream);
+
+/*
  * sv_set_knob -- process-wide test and tuning settings (not needed for
  * normal use; the pages have no counterpart).  Every knob defaults to 0, the
  * library's own choice, and a value set applies to every later call from any
@@ -427,7 +573,8 @@ SV_API sv_status sv_set_knob(int knob, long long value);
  * microseconds of each launch marked since its previous call (at most the
  * last 2048, oldest first, at most `cap`) to us[] and its kind to tags[]
  * (SV_MARK_STREAM: a streaming pass; SV_MARK_FINISH: a finishing or
- * reduction kernel; SV_MARK_CHAIN: the persistent chain kernel), stores the
+ * reduction kernel; SV_MARK_CHAIN: the persistent chain kernel; SV_MARK_KV: a
+ * kernel of the sv_kv_* calls), stores the
  * count in *n and starts a new count.  The marks add an event record between
  * launches, so a marked call can run slightly slower than an unmarked one.
  *   Errors: SV_ERR_INVALID_ARG for null pointers or a current device other
@@ -436,6 +583,7 @@ SV_API sv_status sv_set_knob(int knob, long long value);
 #define SV_MARK_STREAM 0
 #define SV_MARK_FINISH 1
 #define SV_MARK_CHAIN 2
+#define SV_MARK_KV 3
 SV_API sv_status sv_kernel_times(float* us, int32_t* tags, int cap, int32_t* n);
 
 /* Map a device status word (read back by the caller) to a host status:

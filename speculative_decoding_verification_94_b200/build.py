@@ -8,7 +8,7 @@ from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
 CSRC = PKG / "csrc"
-SOURCES = ["sv_api.cu", "sv_chain_bf16.cu", "sv_chain_f32.cu"]
+SOURCES = ["sv_api.cu", "sv_chain_bf16.cu", "sv_chain_f32.cu", "sv_kv.cu"]
 LIB = PKG / "libsv.so"
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",

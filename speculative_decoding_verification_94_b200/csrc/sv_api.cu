@@ -31,7 +31,7 @@ long long g_knobs[kKnobCount];
 // The records are external ones, which stream capture turns into event
 // record nodes, so the calls of a captured graph are timed launch by launch
 // at every replay.
-enum : int { kMarkStream = 0, kMarkFinish = 1, kMarkChain = 2 };
+enum : int { kMarkStream = 0, kMarkFinish = 1, kMarkChain = 2, kMarkKv = 3 };
 constexpr int kMarkLaunches = 2048;
 struct MarkRing {
   cudaEvent_t ev[2 * kMarkLaunches];
@@ -147,6 +147,11 @@ std::mutex g_mu;
 
 }  // namespace
 
+cudaError_t launch_mark_before(cudaStream_t s) { return mark_before(s); }
+cudaError_t launch_mark_after(cudaStream_t s, cudaError_t launched) {
+  return mark_after(s, kMarkKv, launched);
+}
+
 long long knob(int id) {
   if (id < 0 || id >= kKnobCount) return 0;
   return __atomic_load_n(&g_knobs[id], __ATOMIC_RELAXED);
@@ -180,7 +185,7 @@ cudaError_t ensure_kernel_attrs(const void* kernel, int smem_bytes, bool nonport
   return cudaSuccess;
 }
 
-static cudaError_t blocks_per_sm(const void* kernel, int threads, int smem, int* out) {
+cudaError_t blocks_per_sm(const void* kernel, int threads, int smem, int* out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

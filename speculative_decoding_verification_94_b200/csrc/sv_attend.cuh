@@ -1,0 +1,565 @@
+// sv_attend.cuh -- attention of a step's new tokens over the paged cache:
+// the division of the work, the join of split sequences, and the general
+// kernel (any type, head size, stride and alignment).
+//
+// For a request with a committed tokens and m new ones (a chain or a tree),
+// the row of token i and query head x attends to the keys
+//   S_i = [0, a) + {a + j : j is i or an ancestor of i},
+//   o = sum_{j in S_i} e^{z_j - lse} v_j,  z_j = scale q . k_j,
+//   lse = log sum_{j in S_i} e^{z_j}.
+// The rows of all new tokens and of the query heads that share a key head are
+// computed together, so a key is read once for all of them.  The softmax is
+// the running one: a maximum m, a sum l of e^{z - m} and the unnormalised
+// output, all in fp32, rescaled when m grows; parts of a sequence computed
+// apart join by the same rescaling.  Exponentials are powers of two of
+// z log2 e.
+//
+// Division.  The lengths live on the device, so the grid does not know them.
+// A unit is one tile of keys of one (request, key head, row tile); the units
+// of all requests in order are cut into as many equal runs as there are
+// blocks.  A block therefore holds at most two segments that it shares with
+// other blocks, its first and its last; their partial results (output, m, l)
+// go to the workspace, and the last block to arrive at a shared segment joins
+// its parts in block order, so results do not depend on the timing.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "sv_internal.h"
+#include "sv_kv_pages.cuh"
+
+namespace sv {
+
+struct AttendParams {
+  const void* q;
+  const void *k, *v;
+  const int32_t *table, *kv_len, *q_len, *parents;
+  void* out;
+  float* lse;
+  int B, n, hkv, g, d, page, num_pages, max_pages;
+  long long q_b, q_t;                 // strides of q, elements
+  long long c_page, c_token, c_head;  // strides of the cache, elements
+  float scale_log2;
+  uint32_t* counters;  // [grid] arrivals at the segment that starts in block i
+  float* partial;      // [grid][2] partial results
+  int32_t* status;
+};
+
+constexpr int kAttMaxBlocks = 296;  // two blocks on each of 148 SMs
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// A row tile's partial result: o [rows][DP], then m [rows], l [rows].
+__host__ __device__ constexpr int att_partial_floats(int rows, int dp) { return rows * (dp + 2); }
+
+__device__ __forceinline__ float warp_max(float x) {
+  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float warp_add(float x) {
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Lengths of a request: false if they are out of range (the request fails).
+__device__ __forceinline__ bool att_lens(const AttendParams& p, int b, int& kv, int& q) {
+  q = p.q_len ? p.q_len[b] : p.n;
+  kv = p.kv_len[b];
+  if (q == 0) return true;
+  return q > 0 && q <= p.n && kv >= 0 && (long long)kv + q <= (long long)p.max_pages * p.page &&
+         (long long)kv + q <= 0x7fffffffLL;
+}
+
+// The walk over units: requests, then segments (key head, row tile), then
+// tiles of U keys.
+template <int U, int RT>
+struct AttCursor {
+  int b, seg, tile, tiles, mt, kv, q;
+  __device__ __forceinline__ long long load(const AttendParams& p) {  // units of request b
+    tiles = mt = 0;
+    if (b >= p.B || !att_lens(p, b, kv, q) || q == 0) return 0;
+    tiles = (int)(((long long)kv + q + U - 1) / U);
+    mt = (q * p.g + RT - 1) / RT;
+    return (long long)tiles * mt * p.hkv;
+  }
+  __device__ __forceinline__ void place(long long off) {  // off: unit within the request
+    seg = (int)(off / tiles);
+    tile = (int)(off - (long long)seg * tiles);
+  }
+  __device__ __forceinline__ void next_segment(const AttendParams& p) {
+    tile = 0;
+    if (++seg == mt * p.hkv) {
+      seg = 0;
+      do ++b;
+      while (b < p.B && load(p) == 0);
+    }
+  }
+  __device__ __forceinline__ void advance(const AttendParams& p) {
+    if (++tile == tiles) next_segment(p);
+  }
+};
+
+struct AttShare {
+  long long total, u0, u1;  // all units; this block's run
+  int blocks;               // blocks with work
+  __device__ __forceinline__ long long start(int c) const { return total * c / blocks; }
+  __device__ __forceinline__ int block_of(long long u) const {
+    return (int)(((u + 1) * blocks - 1) / total);
+  }
+};
+
+// Every block sums the units of all requests and finds its own run.
+template <int U, int RT, int THREADS>
+__device__ __forceinline__ AttShare att_share(const AttendParams& p, AttCursor<U, RT>& cur) {
+  __shared__ long long s_sum[THREADS / 32 + 1];
+  __shared__ long long s_off;
+  __shared__ int s_b;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.B + THREADS - 1) / THREADS;
+  const int b0 = tid * per;
+  long long sum = 0;
+  for (int j = 0; j < per; ++j) {
+    cur.b = b0 + j;
+    sum += cur.load(p);
+  }
+  long long inc = sum;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += a;
+  }
+  if (lane == 31) s_sum[warp] = inc;
+  __syncthreads();
+  long long total = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) inc += s_sum[w];
+    total += s_sum[w];
+  }
+  AttShare s;
+  s.total = total;
+  s.blocks = total < (long long)gridDim.x ? (int)total : (int)gridDim.x;
+  s.u0 = s.u1 = 0;
+  if ((int)blockIdx.x < s.blocks) {
+    s.u0 = s.start(blockIdx.x);
+    s.u1 = s.start(blockIdx.x + 1);
+    long long at = inc - sum;
+    if (s.u0 >= at && s.u0 < inc) {
+      for (int j = 0; j < per; ++j) {
+        cur.b = b0 + j;
+        const long long u = cur.load(p);
+        if (s.u0 < at + u) {
+          s_b = cur.b;
+          s_off = s.u0 - at;
+          break;
+        }
+        at += u;
+      }
+    }
+  }
+  __syncthreads();
+  if (s.u0 < s.u1) {
+    cur.b = s_b;
+    cur.load(p);
+    cur.place(s_off);
+  }
+  return s;
+}
+
+// Does the row of token i attend to the key at position pos >= kv?  Chains:
+// pos - kv <= i.  Trees: the keys of one tile as bits, found by walking up
+// from i; false in `ok` for a parent that is not an earlier node or -1.
+__device__ __forceinline__ uint32_t att_tree_bits(const int32_t* parents, int i, int lo, int count,
+                                                  bool& ok) {
+  uint32_t bits = 0;
+  int a = i;
+  while (a >= lo) {
+    if (a - lo < count) bits |= 1u << (a - lo);
+    const int up = parents[a];
+    if (up >= a || up < -1) {
+      ok = false;
+      break;
+    }
+    a = up;
+  }
+  return bits;
+}
+
+template <class T>
+__device__ __forceinline__ float to_f32(T x);
+template <>
+__device__ __forceinline__ float to_f32<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) {
+  return __bfloat162float(x);
+}
+template <class T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+__device__ __forceinline__ bool not_finite(float x) {
+  return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u;
+}
+
+// Output row of tile row r: token and query head.
+__device__ __forceinline__ long long att_out_row(const AttendParams& p, int b, int h, int r) {
+  const int i = r / p.g;
+  return ((long long)b * p.n + i) * ((long long)p.hkv * p.g) + (long long)h * p.g + (r - i * p.g);
+}
+
+// Tokens that no row was computed for: zeros and lse -inf for those behind a
+// request's own, NaN for a failed request.
+template <class T, int THREADS>
+__device__ __forceinline__ void att_fill_padding(const AttendParams& p) {
+  const int hq = p.hkv * p.g;
+  const long long tokens = (long long)p.B * p.n;
+  for (long long t = blockIdx.x; t < tokens; t += gridDim.x) {
+    const int b = (int)(t / p.n), i = (int)(t - (long long)b * p.n);
+    int kv, q;
+    const bool ok = att_lens(p, b, kv, q);
+    if (ok && i < q) continue;
+    const float nan = __int_as_float(0x7fc00000);
+    if (!ok && i == 0 && threadIdx.x == 0) kv_flag(p.status, SV_DEV_BAD_LEN);
+    const T z = from_f32<T>(ok ? 0.f : nan);
+    T* o = static_cast<T*>(p.out) + t * hq * p.d;
+    for (int e = threadIdx.x; e < hq * p.d; e += THREADS) o[e] = z;
+    if (p.lse)
+      for (int e = threadIdx.x; e < hq; e += THREADS) p.lse[t * hq + e] = ok ? -INFINITY : nan;
+  }
+}
+
+// Joins the parts of a shared segment.  A warp takes a row; its lanes hold
+// the parts' weights (32 parts at a time) and then the row's DP values.  The
+// parts are set back to zero as they are read.
+template <class T, int DP, int RT, int THREADS>
+__device__ __forceinline__ void att_join(const AttendParams& p, int b, int h, int row0, int rows,
+                                         int c0, int c1) {
+  constexpr int VPL = DP / 32;
+  constexpr int kStride = att_partial_floats(RT, DP);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int parts = c1 - c0 + 1;
+  // a block keeps the part of a segment that starts in it in its second place
+  auto part = [&](int c) { return p.partial + ((long long)c * 2 + (c == c0)) * kStride; };
+  for (int r = warp; r < rows; r += THREADS / 32) {
+    float m = -INFINITY;
+    for (int j = lane; j < parts; j += 32) m = fmaxf(m, __ldcg(part(c0 + j) + RT * DP + r));
+    m = warp_max(m);
+    float l = 0.f, acc[VPL];
+#pragma unroll
+    for (int e = 0; e < VPL; ++e) acc[e] = 0.f;
+    for (int j0 = 0; j0 < parts; j0 += 32) {
+      float w = 0.f;
+      if (j0 + lane < parts) {
+        float* t = part(c0 + j0 + lane) + RT * DP + r;
+        w = exp2f(__ldcg(t) - m);
+        l += w * __ldcg(t + RT);
+        __stcg(t, 0.f);
+        __stcg(t + RT, 0.f);
+      }
+      const int cnt = min(32, parts - j0);
+#pragma unroll 8
+      for (int j = 0; j < cnt; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        float* t = part(c0 + j0 + j) + r * DP + lane * VPL;
+        if constexpr (VPL == 2) {
+          const float2 x = __ldcg(reinterpret_cast<float2*>(t));
+          acc[0] += wj * x.x, acc[1] += wj * x.y;
+          __stcg(reinterpret_cast<float2*>(t), make_float2(0.f, 0.f));
+        } else {
+#pragma unroll
+          for (int e = 0; e < VPL; e += 4) {
+            const float4 x = __ldcg(reinterpret_cast<float4*>(t + e));
+            acc[e] += wj * x.x, acc[e + 1] += wj * x.y;
+            acc[e + 2] += wj * x.z, acc[e + 3] += wj * x.w;
+            __stcg(reinterpret_cast<float4*>(t + e), make_float4(0.f, 0.f, 0.f, 0.f));
+          }
+        }
+      }
+    }
+    l = warp_add(l);
+    const long long o = att_out_row(p, b, h, row0 + r);
+    T* out = static_cast<T*>(p.out) + o * p.d;
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int e = 0; e < VPL; ++e)
+      if (lane * VPL + e < p.d) out[lane * VPL + e] = from_f32<T>(acc[e] * inv);
+    if (lane == 0 && p.lse) p.lse[o] = (m + log2f(l)) * kLn2;
+  }
+}
+
+// After a block's part of a shared segment is in the workspace: counts it, and
+// the last block joins.  `flag` is one shared int.
+template <class T, int DP, int RT, int THREADS>
+__device__ __forceinline__ void att_arrive(const AttendParams& p, const AttShare& s, int b, int h,
+                                           int row0, int rows, long long seg_u0, long long seg_u1,
+                                           int* flag) {
+  const int c0 = s.block_of(seg_u0), c1 = s.block_of(seg_u1 - 1);
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const uint32_t before = atomicAdd(p.counters + c0, 1u);
+    *flag = before == (uint32_t)(c1 - c0);
+    if (*flag) {
+      p.counters[c0] = 0;
+      __threadfence();
+    }
+  }
+  __syncthreads();
+  if (*flag) att_join<T, DP, RT, THREADS>(p, b, h, row0, rows, c0, c1);
+}
+
+// ---------------------------------------------------------------------------
+// The general kernel: fp32 arithmetic throughout, so fp32 caches keep their
+// precision.  32 keys a tile, staged in shared memory as fp32; a lane holds a
+// key and a warp four of the 16 rows while scores are formed, then a thread
+// holds a column of the output.
+// ---------------------------------------------------------------------------
+constexpr int kGenThreads = 128, kGenU = 32, kGenR = 16;
+
+template <int DP>
+struct GenSmem {
+  float k[kGenU][DP + 4];  // +4: a lane per row reads 16 bytes without conflicts
+  float v[kGenU][DP];
+  float q[kGenR][DP];
+  float p[kGenR][kGenU];
+  float alpha[kGenR], m[kGenR], l[kGenR];
+  const unsigned char* row_k[kGenU];
+  const unsigned char* row_v[kGenU];
+  int bad, flag;
+};
+
+template <class T, int DP, bool VEC>
+__global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const AttendParams p) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  GenSmem<DP>& sm = *reinterpret_cast<GenSmem<DP>*>(smem_raw);
+  constexpr int kRG = DP == 64 ? 2 : 1;            // thread groups over the rows
+  constexpr int kRows = kGenR / kRG;               // rows of a thread
+  constexpr int kCols = DP == 256 ? 2 : 1;         // columns of a thread
+  constexpr int kStride = att_partial_floats(kGenR, DP);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int col = tid % (kGenThreads / kRG), rg = tid / (kGenThreads / kRG) * kRows;
+  AttCursor<kGenU, kGenR> cur;
+  const AttShare s = att_share<kGenU, kGenR, kGenThreads>(p, cur);
+  const T* kc = static_cast<const T*>(p.k);
+  const T* vc = static_cast<const T*>(p.v);
+  for (long long u = s.u0; u < s.u1;) {
+    const int h = cur.seg / cur.mt, row0 = (cur.seg % cur.mt) * kGenR;
+    const int rows = min(kGenR, cur.q * p.g - row0);
+    const int tile0 = cur.tile, left = cur.tiles - cur.tile;
+    const int cnt = s.u1 - u < left ? (int)(s.u1 - u) : left;
+    const int len = cur.kv + cur.q;
+    const int32_t* trow = p.table + (long long)cur.b * p.max_pages;
+    const int32_t* par = p.parents ? p.parents + (long long)cur.b * p.n : nullptr;
+    __syncthreads();
+    if (tid == 0) sm.bad = 0;
+    for (int e = tid; e < kGenR * DP; e += kGenThreads) {
+      const int r = e / DP, d = e % DP;
+      float x = 0.f;
+      if (r < rows && d < p.d) {
+        const int i = (row0 + r) / p.g, gi = (row0 + r) - i * p.g;
+        x = to_f32<T>(static_cast<const T*>(p.q)[cur.b * p.q_b + i * p.q_t +
+                                                 (long long)(h * p.g + gi) * p.d + d]);
+      }
+      sm.q[r][d] = x;
+    }
+    float m[4], l[4], acc[kRows * kCols];
+    bool tree_ok = true;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = -INFINITY, l[j] = 0.f;
+#pragma unroll
+    for (int j = 0; j < kRows * kCols; ++j) acc[j] = 0.f;
+    for (int t = tile0; t < tile0 + cnt; ++t) {
+      const int pos0 = t * kGenU;
+      __syncthreads();
+      if (tid < kGenU) {
+        const int pos = pos0 + tid;
+        const unsigned char *rk = nullptr, *rv = nullptr;
+        if (pos < len) {
+          const int pi = pos / p.page;
+          const int id = trow[pi];
+          if (id >= 0 && id < p.num_pages) {
+            const long long at =
+                id * p.c_page + (long long)(pos - pi * p.page) * p.c_token + h * p.c_head;
+            rk = reinterpret_cast<const unsigned char*>(kc + at);
+            rv = reinterpret_cast<const unsigned char*>(vc + at);
+          } else {
+            sm.bad = 1;
+          }
+        }
+        sm.row_k[tid] = rk;
+        sm.row_v[tid] = rv;
+      }
+      __syncthreads();
+      if constexpr (VEC) {
+        constexpr int kPer = 16 / sizeof(T), kCh = DP / kPer;
+        const int nch = p.d / kPer;
+#pragma unroll 4
+        for (int e = tid; e < kGenU * kCh * 2; e += kGenThreads) {
+          const int w = e / (kGenU * kCh), f = e % (kGenU * kCh);
+          const int r = f / kCh, c = f % kCh;
+          const unsigned char* src = w ? sm.row_v[r] : sm.row_k[r];
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (src && c < nch) x = __ldcs(reinterpret_cast<const uint4*>(src) + c);
+          float* dst = (w ? sm.v[r] : sm.k[r]) + c * kPer;
+          if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<uint4*>(dst) = x;
+          } else {
+            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              dst[2 * j] = __uint_as_float(y[j] << 16);
+              dst[2 * j + 1] = __uint_as_float(y[j] & 0xffff0000u);
+            }
+          }
+        }
+      } else {
+        for (int e = tid; e < kGenU * DP * 2; e += kGenThreads) {
+          const int w = e / (kGenU * DP), f = e % (kGenU * DP);
+          const int r = f / DP, d = f % DP;
+          const T* src = reinterpret_cast<const T*>(w ? sm.row_v[r] : sm.row_k[r]);
+          (w ? sm.v[r] : sm.k[r])[d] = (src && d < p.d) ? to_f32<T>(src[d]) : 0.f;
+        }
+      }
+      __syncthreads();
+      // scores: lane = key, rows warp, warp + 4, ...
+      float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int d = 0; d < DP; d += 4) {
+        const float4 kk = *reinterpret_cast<const float4*>(&sm.k[lane][d]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 qq = *reinterpret_cast<const float4*>(&sm.q[warp + 4 * j][d]);
+          z[j] = fmaf(qq.x, kk.x, z[j]);
+          z[j] = fmaf(qq.y, kk.y, z[j]);
+          z[j] = fmaf(qq.z, kk.z, z[j]);
+          z[j] = fmaf(qq.w, kk.w, z[j]);
+        }
+      }
+      const int pos = pos0 + lane;
+      const bool tail = pos0 + kGenU > cur.kv;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = warp + 4 * j;
+        float x = z[j] * p.scale_log2;
+        if (tail) {
+          const int i = min((row0 + r) / p.g, cur.q - 1);
+          bool on = pos < cur.kv || (pos < len && pos - cur.kv <= i);
+          if (par && pos0 + kGenU > cur.kv) {
+            const int lo = pos0 - cur.kv;  // node of the tile's first key
+            const uint32_t bits = lo >= 0 ? att_tree_bits(par, i, lo, kGenU, tree_ok)
+                                          : att_tree_bits(par, i, 0, kGenU + lo, tree_ok) << -lo;
+            on = pos < cur.kv || (bits >> lane & 1u);
+          }
+          if (!on) x = -INFINITY;
+        }
+        const float mn = fmaxf(m[j], warp_max(x));
+        const float ms = mn == -INFINITY ? 0.f : mn;
+        const float a = exp2f(m[j] - ms), pr = exp2f(x - ms);
+        m[j] = mn;
+        l[j] = l[j] * a + pr;
+        sm.p[r][lane] = pr;
+        if (lane == 0) sm.alpha[r] = a;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const float a = sm.alpha[rg + r];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[r * kCols + c] *= a;
+      }
+      if (!tail) {
+#pragma unroll 2
+        for (int key = 0; key < kGenU; key += 4) {
+          float vv[4][kCols];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) vv[x][c] = sm.v[key + x][col + c * kGenThreads];
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) {
+            const float4 pp = *reinterpret_cast<const float4*>(&sm.p[rg + r][key]);
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+              float& o = acc[r * kCols + c];
+              o = fmaf(pp.x, vv[0][c], o);
+              o = fmaf(pp.y, vv[1][c], o);
+              o = fmaf(pp.z, vv[2][c], o);
+              o = fmaf(pp.w, vv[3][c], o);
+            }
+          }
+        }
+      } else {
+        // keys that only some rows see: a weight of zero leaves the row as it
+        // is, whatever the key's value holds
+        for (int key = 0; key < kGenU; ++key)
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) {
+            const float pr = sm.p[rg + r][key];
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+              float& o = acc[r * kCols + c];
+              o = pr == 0.f ? o : fmaf(pr, sm.v[key][col + c * kGenThreads], o);
+            }
+          }
+      }
+    }
+    // this segment's result
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float x = warp_add(l[j]);
+      if (!tree_ok) {
+        x = __int_as_float(0x7fc00000);
+        if (lane == 0 && warp + 4 * j < rows) kv_flag(p.status, SV_DEV_BAD_TREE);
+      }
+      if (lane == 0) sm.m[warp + 4 * j] = m[j], sm.l[warp + 4 * j] = x;
+    }
+    __syncthreads();
+    const bool bad = sm.bad != 0;
+    if (bad && tid == 0) kv_flag(p.status, SV_DEV_BAD_INDEX);
+    const float nan = __int_as_float(0x7fc00000);
+    if (tile0 == 0 && cnt == cur.tiles) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        if (rg + r >= rows) continue;
+        const float ll = bad ? nan : sm.l[rg + r];
+        const long long o = att_out_row(p, cur.b, h, row0 + rg + r);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          const int d = col + c * kGenThreads;
+          if (d < p.d) static_cast<T*>(p.out)[o * p.d + d] = from_f32<T>(acc[r * kCols + c] / ll);
+        }
+        if (col == 0 && p.lse) p.lse[o] = (sm.m[rg + r] + log2f(ll)) * kLn2;
+      }
+    } else {
+      const long long seg_u0 = u - tile0, seg_u1 = seg_u0 + cur.tiles;
+      float* t = p.partial + ((long long)blockIdx.x * 2 + (tile0 == 0 ? 1 : 0)) * kStride;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          if (rg + r < rows) __stcg(t + (rg + r) * DP + col + c * kGenThreads, acc[r * kCols + c]);
+      if (tid < rows) {
+        __stcg(t + kGenR * DP + tid, sm.m[tid]);
+        __stcg(t + kGenR * DP + kGenR + tid, bad ? nan : sm.l[tid]);
+      }
+      att_arrive<T, DP, kGenR, kGenThreads>(p, s, cur.b, h, row0, rows, seg_u0, seg_u1, &sm.flag);
+    }
+    u += cnt;
+    if (tile0 + cnt == cur.tiles)
+      cur.next_segment(p);
+    else
+      cur.tile += cnt;
+  }
+  att_fill_padding<T, kGenThreads>(p);
+}
+
+}  // namespace sv

@@ -39,6 +39,10 @@ long long knob(int id);
 // Per-device helpers shared by the launchers (sv_api.cu).
 cudaError_t ensure_kernel_attrs(const void* kernel, int smem_bytes, bool nonportable);
 cudaError_t sm_count(int* out);
+cudaError_t blocks_per_sm(const void* kernel, int threads, int smem, int* out);
+// Timing marks around a launch of the paged cache's kernels (SV_MARK_KV).
+cudaError_t launch_mark_before(cudaStream_t s);
+cudaError_t launch_mark_after(cudaStream_t s, cudaError_t launched);
 
 // Chain verification in one persistent launch (sv_chain_*.cu): the
 // arguments of sv_verify_chain after validation, the workspace carved by

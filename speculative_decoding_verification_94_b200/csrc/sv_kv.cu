@@ -1,0 +1,322 @@
+// sv_kv.cu -- the paged key-value cache calls of the C ABI: argument checks,
+// choice of kernel and launches.  No entry point synchronises or allocates.
+#include <math.h>
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "sv_attend.cuh"
+#include "sv_kv_pages.cuh"
+
+namespace sv {
+namespace {
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline bool aligned_or_null(const void* p, size_t a) { return aligned(p, a); }
+inline int esize(sv_dtype d) { return d == SV_BF16 ? 2 : 4; }
+inline sv_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
+
+// The widest power of two up to 16 that divides every value.
+int common_width(std::initializer_list<long long> v) {
+  int w = 16;
+  for (long long x : v)
+    while (x % w) w /= 2;
+  return w;
+}
+long long addr(const void* p) { return (long long)(reinterpret_cast<uintptr_t>(p) % 16); }
+
+// Type, sizes, and strides under which no two tokens' rows overlap.
+sv_status check_cache(const sv_kv_cache* c, int layers = 1, long long layer_stride = 0) {
+  if (!c || (c->dtype != SV_F32 && c->dtype != SV_BF16)) return SV_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->page_size < 1 || c->heads < 1 || c->head_dim < 1)
+    return SV_ERR_INVALID_ARG;
+  if (c->head_dim > 256) return SV_ERR_UNSUPPORTED;
+  if (!c->k || !c->v || !aligned(c->k, esize(c->dtype)) || !aligned(c->v, esize(c->dtype)))
+    return SV_ERR_INVALID_ARG;
+  struct Dim {
+    long long stride, extent;
+  } d[4] = {{c->page_stride, c->num_pages}, {c->token_stride, c->page_size},
+            {c->head_stride, c->heads}, {layer_stride, layers}};
+  for (auto& x : d)
+    if (x.stride < 0 || x.stride > (1LL << 44)) return SV_ERR_INVALID_ARG;
+  std::sort(d, d + 4, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  double span = c->head_dim;  // elements from the first to the last of the dimensions so far
+  for (auto& x : d) {
+    if (x.extent == 1) continue;
+    if ((double)x.stride < span) return SV_ERR_INVALID_ARG;
+    span += (double)x.stride * (double)(x.extent - 1);
+  }
+  if (span > 1e18) return SV_ERR_UNSUPPORTED;
+  return SV_OK;
+}
+
+template <class K, class Prm>
+cudaError_t launch(K kernel, const Prm& prm, dim3 grid, int threads, int smem, cudaStream_t s) {
+  cudaError_t e = smem > 48 * 1024
+                      ? ensure_kernel_attrs(reinterpret_cast<const void*>(kernel), smem, false)
+                      : cudaSuccess;
+  if (e != cudaSuccess) return e;
+  if ((e = launch_mark_before(s)) != cudaSuccess) return e;
+  kernel<<<grid, threads, smem, s>>>(prm);
+  return launch_mark_after(s, cudaGetLastError());
+}
+
+// ---------------------------------------------------------------------------
+// Attention: grid and workspace
+// ---------------------------------------------------------------------------
+int padded_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+
+constexpr size_t kCounterBytes = (4 * kAttMaxBlocks + 255) / 256 * 256;
+
+size_t attend_ws(int head_dim) {
+  return kCounterBytes +
+         (size_t)kAttMaxBlocks * 2 * att_partial_floats(kGenR, padded_dim(head_dim)) * 4;
+}
+
+template <class K>
+cudaError_t launch_attend(K kernel, AttendParams& p, int threads, int smem, cudaStream_t s) {
+  const void* kp = reinterpret_cast<const void*>(kernel);
+  cudaError_t e = ensure_kernel_attrs(kp, smem, false);
+  if (e != cudaSuccess) return e;
+  int per_sm = 0, sms = 0;
+  if ((e = blocks_per_sm(kp, threads, smem, &per_sm)) != cudaSuccess) return e;
+  if ((e = sm_count(&sms)) != cudaSuccess) return e;
+  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  const int grid = std::min(per_sm * sms, kAttMaxBlocks);
+  return launch(kernel, p, dim3((unsigned)grid), threads, smem, s);
+}
+
+template <class T, bool VEC>
+cudaError_t launch_general(AttendParams& p, cudaStream_t s) {
+  switch (padded_dim(p.d)) {
+    case 64:
+      return launch_attend(attend_general_kernel<T, 64, VEC>, p, kGenThreads, sizeof(GenSmem<64>), s);
+    case 128:
+      return launch_attend(attend_general_kernel<T, 128, VEC>, p, kGenThreads, sizeof(GenSmem<128>),
+                           s);
+    default:
+      return launch_attend(attend_general_kernel<T, 256, VEC>, p, kGenThreads, sizeof(GenSmem<256>),
+                           s);
+  }
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" {
+
+sv_status sv_kv_plan(const int32_t* kv_len, const int32_t* written, const int32_t* accepted_len,
+                     const int32_t* release, const int32_t* new_len, int B, int max_new,
+                     int page_size, int num_pages, int32_t* block_table, int max_pages,
+                     const int32_t* pages, int32_t* free_pages, const int32_t* free_count,
+                     int32_t* kv_len_out, int32_t* pages_out, int32_t* free_count_out,
+                     int32_t* q_len, int64_t* slot_map, int32_t* positions, int32_t* device_status,
+                     void* stream) {
+  if (B < 0 || max_new < 1 || page_size < 1 || num_pages < 1 || max_pages < 1)
+    return SV_ERR_INVALID_ARG;
+  if (B == 0) {  // no request changes the stack
+    if (!free_count || !free_count_out || !aligned(free_count, 4) || !aligned(free_count_out, 4))
+      return SV_ERR_INVALID_ARG;
+    if (free_count == free_count_out) return SV_OK;
+    return cuda_status(cudaMemcpyAsync(free_count_out, free_count, 4, cudaMemcpyDeviceToDevice,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+  }
+  const void* need[] = {kv_len, new_len,    block_table, pages,          free_pages,
+                        free_count, kv_len_out, pages_out,   free_count_out, q_len};
+  for (const void* x : need)
+    if (!x || !aligned(x, 4)) return SV_ERR_INVALID_ARG;
+  const void* may[] = {written, accepted_len, release, positions, device_status};
+  for (const void* x : may)
+    if (!aligned_or_null(x, 4)) return SV_ERR_INVALID_ARG;
+  if (!slot_map || !aligned(slot_map, 8)) return SV_ERR_INVALID_ARG;
+  if (accepted_len && !written) return SV_ERR_INVALID_ARG;
+  if (B > kPlanMaxB || (long long)B * max_pages > 0x7fffffffLL ||
+      (long long)B * max_new > 0x7fffffffLL)
+    return SV_ERR_UNSUPPORTED;
+  const PlanParams p = {kv_len, written,   accepted_len, release,    new_len,   pages,
+                        free_count, B,     max_new,      page_size,  num_pages, max_pages,
+                        block_table, free_pages, kv_len_out, pages_out, free_count_out, q_len,
+                        slot_map, positions, device_status,
+                        (long long)B * max_new <= kPlanInlineSlots};
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch(kv_plan_kernel, p, dim3(1), kPlanThreads, (int)plan_smem(B), s);
+  if (e != cudaSuccess) return SV_ERR_CUDA;
+  if (!p.write_slots) {
+    constexpr int kPerBlock = kSlotThreads * kSlotPer;
+    e = launch(kv_plan_slots_kernel, p,
+               dim3((unsigned)((max_new + kPerBlock - 1) / kPerBlock), (unsigned)B), kSlotThreads,
+               0, s);
+  }
+  return cuda_status(e);
+}
+
+sv_status sv_kv_append(const sv_kv_cache* cache, const void* k, const void* v, int B, int n,
+                       int64_t batch_stride, int64_t token_stride, const int64_t* slot_map,
+                       int32_t* device_status, void* stream) {
+  if (B < 0 || n < 1) return SV_ERR_INVALID_ARG;
+  const sv_status st = check_cache(cache);
+  if (st != SV_OK) return st;
+  if (batch_stride < 0 || token_stride < 0) return SV_ERR_INVALID_ARG;
+  if (B == 0) return SV_OK;
+  const int es = esize(cache->dtype);
+  if (!k || !v || !slot_map || !aligned(k, es) || !aligned(v, es) || !aligned(slot_map, 8) ||
+      !aligned_or_null(device_status, 4))
+    return SV_ERR_INVALID_ARG;
+  if (batch_stride > (1LL << 40) || token_stride > (1LL << 40)) return SV_ERR_INVALID_ARG;
+  AppendParams p = {};
+  p.k = static_cast<const unsigned char*>(k);
+  p.v = static_cast<const unsigned char*>(v);
+  p.kc = static_cast<unsigned char*>(cache->k);
+  p.vc = static_cast<unsigned char*>(cache->v);
+  p.in_b = batch_stride * es;
+  p.in_t = token_stride * es;
+  p.c_page = cache->page_stride * es;
+  p.c_token = cache->token_stride * es;
+  p.c_head = cache->head_stride * es;
+  p.slot_map = slot_map;
+  p.B = B;
+  p.n = n;
+  p.heads = cache->heads;
+  p.page = cache->page_size;
+  p.num_pages = cache->num_pages;
+  p.status = device_status;
+  const long long row = (long long)cache->head_dim * es;
+  const int w = common_width({addr(k), addr(v), addr(cache->k), addr(cache->v), p.in_b, p.in_t,
+                              p.c_page, p.c_token, p.c_head, row});
+  p.head_chunks = (int)(row / w);
+  int sms = 0;
+  if (sm_count(&sms) != cudaSuccess) return SV_ERR_CUDA;
+  const long long warps = (long long)B * n;
+  const unsigned grid = (unsigned)std::min<long long>((warps + 7) / 8, (long long)sms * 8);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (w) {
+    case 16: return cuda_status(launch(kv_append_kernel<uint4>, p, dim3(grid), 256, 0, s));
+    case 8: return cuda_status(launch(kv_append_kernel<uint2>, p, dim3(grid), 256, 0, s));
+    case 4: return cuda_status(launch(kv_append_kernel<uint32_t>, p, dim3(grid), 256, 0, s));
+    default: return cuda_status(launch(kv_append_kernel<uint16_t>, p, dim3(grid), 256, 0, s));
+  }
+}
+
+size_t sv_kv_attend_workspace_size(int B, int n, int q_heads, int heads, int head_dim,
+                                   sv_dtype dtype) {
+  if (B < 0 || n < 1 || heads < 1 || q_heads < 1 || head_dim < 1 || head_dim > 256 ||
+      (dtype != SV_F32 && dtype != SV_BF16))
+    return 0;
+  return attend_ws(head_dim);
+}
+
+sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_stride,
+                       int64_t token_stride, int B, int n, int q_heads, const int32_t* block_table,
+                       int max_pages, const int32_t* kv_len, const int32_t* q_len,
+                       const int32_t* parents, float scale, void* out, float* lse, void* workspace,
+                       size_t workspace_bytes, int32_t* device_status, void* stream) {
+  if (B < 0 || n < 1 || n > 1024 || q_heads < 1 || max_pages < 1) return SV_ERR_INVALID_ARG;
+  const sv_status st = check_cache(cache);
+  if (st != SV_OK) return st;
+  if (q_heads % cache->heads) return SV_ERR_INVALID_ARG;
+  if (!isfinite(scale) || !isfinite(scale * 1.4426950408889634f)) return SV_ERR_INVALID_ARG;
+  if (batch_stride < 0 || token_stride < 0 || batch_stride > (1LL << 40) ||
+      token_stride > (1LL << 40))
+    return SV_ERR_INVALID_ARG;
+  if (B == 0) return SV_OK;
+  const int es = esize(cache->dtype);
+  if (!q || !out || !block_table || !kv_len || !aligned(q, es) || !aligned(out, es) ||
+      !aligned(block_table, 4) || !aligned(kv_len, 4) || !aligned_or_null(q_len, 4) ||
+      !aligned_or_null(parents, 4) || !aligned_or_null(lse, 4) ||
+      !aligned_or_null(device_status, 4))
+    return SV_ERR_INVALID_ARG;
+  if (q_heads > (1 << 16) || (long long)B * n > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < attend_ws(cache->head_dim))
+    return SV_ERR_WORKSPACE;
+  AttendParams p = {};
+  p.q = q;
+  p.k = cache->k;
+  p.v = cache->v;
+  p.table = block_table;
+  p.kv_len = kv_len;
+  p.q_len = q_len;
+  p.parents = parents;
+  p.out = out;
+  p.lse = lse;
+  p.B = B;
+  p.n = n;
+  p.hkv = cache->heads;
+  p.g = q_heads / cache->heads;
+  p.d = cache->head_dim;
+  p.page = cache->page_size;
+  p.num_pages = cache->num_pages;
+  p.max_pages = max_pages;
+  p.q_b = batch_stride;
+  p.q_t = token_stride;
+  p.c_page = cache->page_stride;
+  p.c_token = cache->token_stride;
+  p.c_head = cache->head_stride;
+  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.counters = static_cast<uint32_t*>(workspace);
+  p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kCounterBytes);
+  p.status = device_status;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool vec = common_width({addr(cache->k), addr(cache->v), p.c_page * es, p.c_token * es,
+                                 p.c_head * es, (long long)p.d * es}) == 16;
+  cudaError_t e;
+  if (cache->dtype == SV_BF16)
+    e = vec ? launch_general<__nv_bfloat16, true>(p, s) : launch_general<__nv_bfloat16, false>(p, s);
+  else
+    e = vec ? launch_general<float, true>(p, s) : launch_general<float, false>(p, s);
+  return cuda_status(e);
+}
+
+sv_status sv_kv_commit(const sv_kv_cache* cache, int layers, int64_t layer_stride, int B,
+                       const int32_t* block_table, int max_pages, const int32_t* kv_len,
+                       const int32_t* accepted_nodes, int width, const int32_t* accepted_len,
+                       int32_t* device_status, void* stream) {
+  if (B < 0 || layers < 1 || layer_stride < 0 || max_pages < 1 || width < 1)
+    return SV_ERR_INVALID_ARG;
+  const sv_status st = check_cache(cache, layers, layer_stride);
+  if (st != SV_OK) return st;
+  if (width > kCommitMaxWidth || B > 65535) return SV_ERR_UNSUPPORTED;
+  if (B == 0) return SV_OK;
+  if (!block_table || !kv_len || !accepted_nodes || !accepted_len || !aligned(block_table, 4) ||
+      !aligned(kv_len, 4) || !aligned(accepted_nodes, 4) || !aligned(accepted_len, 4) ||
+      !aligned_or_null(device_status, 4))
+    return SV_ERR_INVALID_ARG;
+  const int es = esize(cache->dtype);
+  CommitParams p = {};
+  p.kc = static_cast<unsigned char*>(cache->k);
+  p.vc = static_cast<unsigned char*>(cache->v);
+  p.c_layer = layer_stride * es;
+  p.c_page = cache->page_stride * es;
+  p.c_token = cache->token_stride * es;
+  p.c_head = cache->head_stride * es;
+  p.table = block_table;
+  p.kv_len = kv_len;
+  p.nodes = accepted_nodes;
+  p.accepted = accepted_len;
+  p.B = B;
+  p.width = width;
+  p.layers = layers;
+  p.heads = cache->heads;
+  p.page = cache->page_size;
+  p.num_pages = cache->num_pages;
+  p.max_pages = max_pages;
+  p.status = device_status;
+  const long long row = (long long)cache->head_dim * es;
+  const int w = common_width(
+      {addr(cache->k), addr(cache->v), p.c_layer, p.c_page, p.c_token, p.c_head, row});
+  p.head_chunks = (int)(row / w);
+  const long long items = 2LL * layers * cache->heads * p.head_chunks;
+  const long long blocks = (items + kCommitThreads - 1) / kCommitThreads;
+  if (blocks > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)blocks, (unsigned)B);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (w) {
+    case 16: return cuda_status(launch(kv_commit_kernel<uint4>, p, grid, kCommitThreads, 0, s));
+    case 8: return cuda_status(launch(kv_commit_kernel<uint2>, p, grid, kCommitThreads, 0, s));
+    case 4: return cuda_status(launch(kv_commit_kernel<uint32_t>, p, grid, kCommitThreads, 0, s));
+    default: return cuda_status(launch(kv_commit_kernel<uint16_t>, p, grid, kCommitThreads, 0, s));
+  }
+}
+
+}  // extern "C"

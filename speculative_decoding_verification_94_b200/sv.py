@@ -24,14 +24,16 @@ SV_DRAFT_LOGITS, SV_DRAFT_PROBS = 0, 1
 SV_W_RAW, SV_W_GROUP_NORM = 0, 1
 SV_DEV_BAD_TOKEN, SV_DEV_NO_FINITE, SV_DEV_TIMEOUT, SV_DEV_BAD_TREE = 0x1, 0x2, 0x4, 0x8
 SV_DEV_BAD_INDEX, SV_DEV_BAD_LEN, SV_DEV_ERROR_MASK = 0x10, 0x20, 0xFF
+SV_DEV_NO_PAGES = 0x40
 SV_DEV_RESIDUAL_ZERO, SV_DEV_TOPK_SLOW = 0x100, 0x200
 
 SV_KNOB_CLUSTER_CTAS, SV_KNOB_STREAM_COUNT, SV_KNOB_STREAM_W, SV_KNOB_WAIT_NS = 1, 2, 3, 4
 SV_KNOB_STALL, SV_KNOB_STAGES, SV_KNOB_ORDER, SV_KNOB_PERSISTENT = 5, 6, 7, 8
 SV_KNOB_KERNEL_MARKS = 9
 SV_KNOB_FINISH_READ = 10
-SV_MARK_STREAM, SV_MARK_FINISH, SV_MARK_CHAIN = 0, 1, 2
-MARK_NAMES = {SV_MARK_STREAM: "stream", SV_MARK_FINISH: "finish", SV_MARK_CHAIN: "chain"}
+SV_MARK_STREAM, SV_MARK_FINISH, SV_MARK_CHAIN, SV_MARK_KV = 0, 1, 2, 3
+MARK_NAMES = {SV_MARK_STREAM: "stream", SV_MARK_FINISH: "finish", SV_MARK_CHAIN: "chain",
+              SV_MARK_KV: "kv"}
 
 EXPORTS = ("sv_verify_chain", "sv_verify_chain_ragged", "sv_verify_chain_noalloc", "sv_set_knob",
            "sv_kernel_times",
@@ -39,6 +41,8 @@ EXPORTS = ("sv_verify_chain", "sv_verify_chain_ragged", "sv_verify_chain_noalloc
            "sv_verify_tree_sample", "sv_extract_topk_kd", "sv_kd_kl_loss", "sv_sched_select",
            "sv_verify_chain_workspace_size", "sv_verify_tree_workspace_size",
            "sv_extract_topk_workspace_size", "sv_kd_kl_loss_workspace_size",
+           "sv_kv_plan", "sv_kv_append", "sv_kv_attend", "sv_kv_attend_workspace_size",
+           "sv_kv_commit",
            "sv_device_status_check", "sv_status_string", "sv_version")
 
 
@@ -55,6 +59,14 @@ class sv_kd_args(ctypes.Structure):
                 ("wmode", ctypes.c_int), ("group", ctypes.c_int), ("clip", ctypes.c_float),
                 ("loss", ctypes.c_void_p), ("total", ctypes.c_void_p),
                 ("positions", ctypes.c_int)]
+
+
+class sv_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -109,6 +121,17 @@ def lib() -> ctypes.CDLL:
             L.sv_verify_tree_sample.restype = ci
             L.sv_sched_select.argtypes = [vp, vp, ci, ci, ci, ci, vp, vp]
             L.sv_sched_select.restype = ci
+            i64 = ctypes.c_int64
+            L.sv_kv_plan.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, vp, ci, vp, vp, vp, vp,
+                                     vp, vp, vp, vp, vp, vp, vp]
+            L.sv_kv_append.argtypes = [vp, vp, vp, ci, ci, i64, i64, vp, vp, vp]
+            L.sv_kv_attend.argtypes = [vp, vp, i64, i64, ci, ci, ci, vp, ci, vp, vp, vp, cf, vp,
+                                       vp, vp, sz, vp, vp]
+            L.sv_kv_commit.argtypes = [vp, ci, i64, ci, vp, ci, vp, vp, ci, vp, vp, vp]
+            L.sv_kv_attend_workspace_size.argtypes = [ci, ci, ci, ci, ci, ci]
+            L.sv_kv_attend_workspace_size.restype = sz
+            for f in ("sv_kv_plan", "sv_kv_append", "sv_kv_attend", "sv_kv_commit"):
+                getattr(L, f).restype = ci
             L.sv_set_knob.argtypes = [ci, ctypes.c_longlong]
             L.sv_set_knob.restype = ci
             L.sv_kernel_times.argtypes = [vp, vp, ci, vp]
@@ -523,3 +546,209 @@ def sv_kd_grad(topk_logp: torch.Tensor, topk_idx: torch.Tensor, draft: torch.Ten
                           _stream(dev, stream))
     _check(rc, "sv_kd_grad")
     return g
+
+
+# ---------------------------------------------------------------------------
+# The paged key-value cache of a verification step
+# ---------------------------------------------------------------------------
+_KV_WS: dict = {}  # (device, stream) -> workspace of the calls on that stream
+
+
+def _on(dev: torch.device, stream):
+    """Context of a call: `dev` is the current device, which the C calls use,
+    and `stream`, if given, the stream of what the binding allocates."""
+    return torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream)
+
+
+def _kv_workspace(dev: torch.device, stream: int, nbytes: int) -> torch.Tensor:
+    """Zero-filled workspace for one call.  Calls on one stream run in order,
+    so they share a buffer; a captured call gets its own, from the graph's
+    memory and zeroed by the graph, since graphs may be replayed anywhere."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+    key = (dev.index, stream)
+    cur = _KV_WS.get(key)
+    if cur is None or cur.numel() < nbytes:
+        cur = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        _KV_WS[key] = cur
+    return cur
+
+
+def _ptr(t, name: str, dtype, dev, numel: int | None = None):
+    """Data pointer of a dense device tensor (None stays None), checked."""
+    if t is None:
+        return None
+    _dev(t, name, dtype)
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} entries, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _kv_cache(k: torch.Tensor, v: torch.Tensor) -> sv_kv_cache:
+    """Descriptor of caches [num_pages, page_size, heads, head_dim]: any
+    strides (the same for both) with a dense last dimension."""
+    for t, name in ((k, "k_cache"), (v, "v_cache")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+        raise ValueError("k_cache and v_cache must be [num_pages, page_size, heads, head_dim] of "
+                         "one shape, type and device")
+    if k.stride() != v.stride() or (k.stride(3) != 1 and k.shape[3] > 1):
+        raise ValueError("k_cache and v_cache must have the same strides and dense rows")
+    return sv_kv_cache(k.data_ptr(), v.data_ptr(), _dtype_code(k), *k.shape, *k.stride()[:3])
+
+
+def _token_rows(t: torch.Tensor, name: str, cache: torch.Tensor, heads: int | None):
+    """Batch and token strides of [B, n, heads, head_dim] with dense tokens."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != 4 or t.shape[3] != cache.shape[-1] or (heads and t.shape[2] != heads):
+        raise ValueError(f"{name} must be [B, n, heads, head_dim] matching the cache, got "
+                         f"{tuple(t.shape)}")
+    if t.dtype != cache.dtype or t.device != cache.device:
+        raise ValueError(f"{name} must have the cache's type and device")
+    d = t.shape[3]
+    if (d > 1 and t.stride(3) != 1) or (t.shape[2] > 1 and t.stride(2) != d):
+        raise ValueError(f"the heads of a token of {name} must be dense")
+    return t.stride(0), t.stride(1)
+
+
+def sv_kv_plan(kv_len: torch.Tensor, block_table: torch.Tensor, pages: torch.Tensor,
+               free_pages: torch.Tensor, free_count: torch.Tensor, new_len: torch.Tensor,
+               max_new: int, page_size: int, *, written: torch.Tensor | None = None,
+               accepted_len: torch.Tensor | None = None, release: torch.Tensor | None = None,
+               out: dict | None = None, device_status: torch.Tensor | None = None,
+               stream=None) -> dict:
+    """Commit the last step, give back and take pages, and map the new tokens
+    to slots (see sv.h).  block_table [B, max_pages] and free_pages change in
+    place.  Returns kv_len, pages, free_count, q_len, slot_map and positions
+    (allocated unless given in `out`, where the first four may be inputs)."""
+    _dev(kv_len, "kv_len", torch.int32)
+    dev = kv_len.device
+    B, i32 = kv_len.numel(), torch.int32
+    _dev(block_table, "block_table", i32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_pages]")
+    o = dict(out) if out else {}
+    with _on(dev, stream):
+        for name, shape, dt in (("kv_len", (B,), i32), ("pages", (B,), i32),
+                                ("free_count", (1,), i32), ("q_len", (B,), i32),
+                                ("slot_map", (B, max_new), torch.int64),
+                                ("positions", (B, max_new), i32)):
+            if name not in o:
+                o[name] = torch.empty(shape, dtype=dt, device=dev)
+    args = (kv_len.data_ptr(), _ptr(written, "written", i32, dev, B),
+            _ptr(accepted_len, "accepted_len", i32, dev, B), _ptr(release, "release", i32, dev, B),
+            _ptr(new_len, "new_len", i32, dev, B), B, int(max_new), int(page_size),
+            free_pages.numel(), _ptr(block_table, "block_table", i32, dev), block_table.shape[1],
+            _ptr(pages, "pages", i32, dev, B), _ptr(free_pages, "free_pages", i32, dev),
+            _ptr(free_count, "free_count", i32, dev, 1), _ptr(o["kv_len"], "kv_len", i32, dev, B),
+            _ptr(o["pages"], "pages", i32, dev, B),
+            _ptr(o["free_count"], "free_count", i32, dev, 1),
+            _ptr(o["q_len"], "q_len", i32, dev, B),
+            _ptr(o["slot_map"], "slot_map", torch.int64, dev, B * max_new),
+            _ptr(o["positions"], "positions", i32, dev, B * max_new),
+            _ptr(device_status, "device_status", i32, dev))
+    with _on(dev, stream):
+        _check(lib().sv_kv_plan(*args, _stream(dev, stream)), "sv_kv_plan")
+    return o
+
+
+def sv_kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cache: torch.Tensor,
+                 v_cache: torch.Tensor, *, device_status: torch.Tensor | None = None,
+                 stream=None) -> None:
+    """Write new tokens' keys and values [B, n, heads, head_dim] to their
+    slots (slot_map [B, n] int64, negative: none) of the caches [num_pages,
+    page_size, heads, head_dim] (see sv.h)."""
+    c = _kv_cache(k_cache, v_cache)
+    dev = k_cache.device
+    st = _token_rows(k, "k", k_cache, k_cache.shape[2])
+    if _token_rows(v, "v", k_cache, k_cache.shape[2]) != st or v.shape != k.shape:
+        raise ValueError("k and v must have the same shape and strides")
+    B, n = k.shape[:2]
+    args = (ctypes.byref(c), k.data_ptr(), v.data_ptr(), B, n, st[0], st[1],
+            _ptr(slot_map, "slot_map", torch.int64, dev, B * n),
+            _ptr(device_status, "device_status", torch.int32, dev))
+    with _on(dev, stream):
+        _check(lib().sv_kv_append(*args, _stream(dev, stream)), "sv_kv_append")
+
+
+def sv_kv_attend_workspace_size(B: int, n: int, q_heads: int, heads: int, head_dim: int,
+                                dtype: torch.dtype) -> int:
+    code = SV_BF16 if dtype == torch.bfloat16 else SV_F32
+    return int(lib().sv_kv_attend_workspace_size(B, n, q_heads, heads, head_dim, code))
+
+
+def sv_kv_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 block_table: torch.Tensor, kv_len: torch.Tensor, *,
+                 q_len: torch.Tensor | None = None, parents: torch.Tensor | None = None,
+                 scale: float | None = None, out: dict | None = None,
+                 ws: torch.Tensor | None = None, device_status: torch.Tensor | None = None,
+                 stream=None) -> dict:
+    """Attention of the new tokens q [B, n, q_heads, head_dim] (a chain, or a
+    tree given by parents [B, n]) over the paged cache (see sv.h).  Returns
+    out [B, n, q_heads, head_dim] and lse [B, n, q_heads].  scale defaults to
+    head_dim ** -0.5."""
+    c = _kv_cache(k_cache, v_cache)
+    dev, i32 = k_cache.device, torch.int32
+    st = _token_rows(q, "q", k_cache, None)
+    B, n, hq, d = q.shape
+    _dev(block_table, "block_table", i32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_pages]")
+    o = dict(out) if out else {}
+    with _on(dev, stream):
+        if "out" not in o:
+            o["out"] = torch.empty(B, n, hq, d, dtype=q.dtype, device=dev)
+        if "lse" not in o:
+            o["lse"] = torch.empty(B, n, hq, dtype=torch.float32, device=dev)
+        s = _stream(dev, stream)
+        if ws is None:
+            nbytes = lib().sv_kv_attend_workspace_size(B, n, hq, k_cache.shape[2], d, c.dtype)
+            ws = _kv_workspace(dev, s.value, nbytes)
+        _check(lib().sv_kv_attend(
+            ctypes.byref(c), q.data_ptr(), st[0], st[1], B, n, hq,
+            _ptr(block_table, "block_table", i32, dev), block_table.shape[1],
+            _ptr(kv_len, "kv_len", i32, dev, B), _ptr(q_len, "q_len", i32, dev, B),
+            _ptr(parents, "parents", i32, dev, B * n),
+            float(d ** -0.5 if scale is None else scale),
+            _ptr(o["out"], "out", q.dtype, dev, q.numel()),
+            _ptr(o["lse"], "lse", torch.float32, dev, B * n * hq), ws.data_ptr(), ws.numel(),
+            _ptr(device_status, "device_status", i32, dev), s), "sv_kv_attend")
+    return o
+
+
+def sv_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                 kv_len: torch.Tensor, accepted_nodes: torch.Tensor, accepted_len: torch.Tensor,
+                 *, device_status: torch.Tensor | None = None, stream=None) -> None:
+    """Move accepted tree paths to the front of their step's tokens (see sv.h).
+    Caches [num_pages, page_size, heads, head_dim] of one layer, or [layers,
+    ...] of all of them; accepted_nodes [B, max_depth + 1] and accepted_len
+    [B] as sv_verify_tree_* return them."""
+    layers, layer_stride = 1, 0
+    k0, v0 = k_cache, v_cache
+    if isinstance(k_cache, torch.Tensor) and isinstance(v_cache, torch.Tensor) and \
+            k_cache.dim() == 5 and v_cache.dim() == 5:
+        layers, layer_stride = k_cache.shape[0], k_cache.stride(0)
+        if v_cache.shape[0] != layers or (layers > 1 and v_cache.stride(0) != layer_stride):
+            raise ValueError("k_cache and v_cache must have the same layers")
+        if layers == 0:
+            return
+        k0, v0 = k_cache[0], v_cache[0]
+    c = _kv_cache(k0, v0)
+    dev, i32 = k0.device, torch.int32
+    B = kv_len.numel()
+    for t, name in ((block_table, "block_table"), (accepted_nodes, "accepted_nodes")):
+        _dev(t, name, i32)
+        if t.dim() != 2 or t.shape[0] != B:
+            raise ValueError(f"{name} must be a matrix of {B} rows")
+    args = (ctypes.byref(c), layers, layer_stride, B,
+            _ptr(block_table, "block_table", i32, dev), block_table.shape[1],
+            _ptr(kv_len, "kv_len", i32, dev, B),
+            _ptr(accepted_nodes, "accepted_nodes", i32, dev), accepted_nodes.shape[1],
+            _ptr(accepted_len, "accepted_len", i32, dev, B),
+            _ptr(device_status, "device_status", i32, dev))
+    with _on(dev, stream):
+        _check(lib().sv_kv_commit(*args, _stream(dev, stream)), "sv_kv_commit")
