@@ -49,6 +49,7 @@ struct AttendParams {
 };
 
 constexpr int kAttMaxBlocks = 296;  // two blocks on each of 148 SMs
+constexpr long long kAttMaxLen = 0x7fffff00;  // a tile past the end still has int positions
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // A row tile's partial result: o [rows][DP], then m [rows], l [rows].
@@ -69,7 +70,7 @@ __device__ __forceinline__ bool att_lens(const AttendParams& p, int b, int& kv, 
   kv = p.kv_len[b];
   if (q == 0) return true;
   return q > 0 && q <= p.n && kv >= 0 && (long long)kv + q <= (long long)p.max_pages * p.page &&
-         (long long)kv + q <= 0x7fffffffLL;
+         (long long)kv + q <= kAttMaxLen;
 }
 
 // The walk over units: requests, then segments (key head, row tile), then

@@ -6,6 +6,7 @@
 #include <initializer_list>
 
 #include "sv_attend.cuh"
+#include "sv_attend_mma.cuh"
 #include "sv_kv_pages.cuh"
 
 namespace sv {
@@ -68,9 +69,11 @@ int padded_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
 constexpr size_t kCounterBytes = (4 * kAttMaxBlocks + 255) / 256 * 256;
 
-size_t attend_ws(int head_dim) {
+// Enough for either kernel: 32 rows at most, 16 in the general one.
+size_t attend_ws(int head_dim, sv_dtype dt) {
+  const int rows = dt == SV_BF16 && (head_dim == 64 || head_dim == 128) ? 32 : kGenR;
   return kCounterBytes +
-         (size_t)kAttMaxBlocks * 2 * att_partial_floats(kGenR, padded_dim(head_dim)) * 4;
+         (size_t)kAttMaxBlocks * 2 * att_partial_floats(rows, padded_dim(head_dim)) * 4;
 }
 
 template <class K>
@@ -98,6 +101,14 @@ cudaError_t launch_general(AttendParams& p, cudaStream_t s) {
       return launch_attend(attend_general_kernel<T, 256, VEC>, p, kGenThreads, sizeof(GenSmem<256>),
                            s);
   }
+}
+
+template <int D>
+cudaError_t launch_mma(AttendParams& p, cudaStream_t s) {
+  // a second row tile of 16 only where there are rows for it
+  if (p.n * p.g <= 16)
+    return launch_attend(attend_mma_kernel<D, 1>, p, kMmaThreads, MmaCfg<D, 1>::kSmem, s);
+  return launch_attend(attend_mma_kernel<D, 2>, p, kMmaThreads, MmaCfg<D, 2>::kSmem, s);
 }
 
 }  // namespace
@@ -204,7 +215,7 @@ size_t sv_kv_attend_workspace_size(int B, int n, int q_heads, int heads, int hea
   if (B < 0 || n < 1 || heads < 1 || q_heads < 1 || head_dim < 1 || head_dim > 256 ||
       (dtype != SV_F32 && dtype != SV_BF16))
     return 0;
-  return attend_ws(head_dim);
+  return attend_ws(head_dim, dtype);
 }
 
 sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_stride,
@@ -228,7 +239,7 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_st
       !aligned_or_null(device_status, 4))
     return SV_ERR_INVALID_ARG;
   if (q_heads > (1 << 16) || (long long)B * n > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
-  if (!workspace || !aligned(workspace, 16) || workspace_bytes < attend_ws(cache->head_dim))
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < attend_ws(cache->head_dim, cache->dtype))
     return SV_ERR_WORKSPACE;
   AttendParams p = {};
   p.q = q;
@@ -260,8 +271,15 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_st
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool vec = common_width({addr(cache->k), addr(cache->v), p.c_page * es, p.c_token * es,
                                  p.c_head * es, (long long)p.d * es}) == 16;
+  // The matrix kernels take 16-byte rows of the cache and of out, and q in pairs.
+  const bool pairs = common_width({addr(q), p.q_b * es, p.q_t * es}) >= 4 &&
+                     aligned(out, 16);
   cudaError_t e;
-  if (cache->dtype == SV_BF16)
+  if (cache->dtype == SV_BF16 && vec && pairs && p.d == 128)
+    e = launch_mma<128>(p, s);
+  else if (cache->dtype == SV_BF16 && vec && pairs && p.d == 64)
+    e = launch_mma<64>(p, s);
+  else if (cache->dtype == SV_BF16)
     e = vec ? launch_general<__nv_bfloat16, true>(p, s) : launch_general<__nv_bfloat16, false>(p, s);
   else
     e = vec ? launch_general<float, true>(p, s) : launch_general<float, false>(p, s);
