@@ -28,6 +28,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "sv_device.cuh"
 #include "sv_internal.h"
 #include "sv_kv_pages.cuh"
 
@@ -55,10 +56,6 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // A row tile's partial result: o [rows][DP], then m [rows], l [rows].
 __host__ __device__ constexpr int att_partial_floats(int rows, int dp) { return rows * (dp + 2); }
 
-__device__ __forceinline__ float warp_max(float x) {
-  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
 __device__ __forceinline__ float warp_add(float x) {
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
@@ -111,12 +108,16 @@ struct AttShare {
   }
 };
 
-// Every block sums the units of all requests and finds its own run.
+// Every block sums the units of all requests and finds its own run.  `scratch`
+// is kShareBytes of shared memory.
+constexpr int kShareBytes = 128;
 template <int U, int RT, int THREADS>
-__device__ __forceinline__ AttShare att_share(const AttendParams& p, AttCursor<U, RT>& cur) {
-  __shared__ long long s_sum[THREADS / 32 + 1];
-  __shared__ long long s_off;
-  __shared__ int s_b;
+__device__ __forceinline__ AttShare att_share(const AttendParams& p, AttCursor<U, RT>& cur,
+                                              void* scratch) {
+  static_assert(8 * (THREADS / 32 + 2) <= kShareBytes, "");
+  long long* s_sum = static_cast<long long*>(scratch);
+  long long& s_off = s_sum[THREADS / 32];
+  int& s_b = *reinterpret_cast<int*>(s_sum + THREADS / 32 + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + THREADS - 1) / THREADS;
   const int b0 = tid * per;
@@ -336,6 +337,7 @@ struct GenSmem {
   const unsigned char* row_k[kGenU];
   const unsigned char* row_v[kGenU];
   int bad, flag;
+  alignas(16) unsigned char share[kShareBytes];
 };
 
 template <class T, int DP, bool VEC>
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const Atten
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int col = tid % (kGenThreads / kRG), rg = tid / (kGenThreads / kRG) * kRows;
   AttCursor<kGenU, kGenR> cur;
-  const AttShare s = att_share<kGenU, kGenR, kGenThreads>(p, cur);
+  const AttShare s = att_share<kGenU, kGenR, kGenThreads>(p, cur, sm.share);
   const T* kc = static_cast<const T*>(p.k);
   const T* vc = static_cast<const T*>(p.v);
   for (long long u = s.u0; u < s.u1;) {

@@ -37,9 +37,6 @@ struct MmaCfg {
   static constexpr int kSmem = kRing + kMerge + 16;  // two blocks an SM
 };
 
-__device__ __forceinline__ uint32_t s_addr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
 // 16 bytes, or zeros.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -79,8 +76,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 __device__ __forceinline__ bool bf16x2_not_finite(uint32_t x) {
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
@@ -113,7 +108,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
   constexpr int kChunks = D / 8;              // 16-byte chunks of a row
   constexpr int kPerCopy = 32 / kChunks;      // rows that a warp's 32 lanes copy at once
   constexpr int kPart = att_partial_floats(kRows, D);
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   unsigned char* ring = smem + warp * kStages * C::kStage;
   float* merge = reinterpret_cast<float*>(smem + C::kRing);
@@ -123,7 +118,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
   const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(p.v);
 
   AttCursor<kMmaU, kRows> cur;
-  const AttShare s = att_share<kMmaU, kRows, kMmaThreads>(p, cur);
+  const AttShare s = att_share<kMmaU, kRows, kMmaThreads>(p, cur, merge);
 
   // ---- the copies: they run kStages - 1 tiles ahead of the products ---------
   AttCursor<kMmaU, kRows> ahead = cur;
@@ -146,7 +141,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
         at = page * p.c_page + (long long)(pos % p.page) * p.c_token + h * p.c_head;
       const bool bad = __any_sync(0xffffffffu, page == -2);
       bad_stages = (bad_stages & ~(1u << stage)) | ((uint32_t)bad << stage);
-      const uint32_t dst = s_addr(ring + stage * C::kStage);
+      const uint32_t dst = smem_u32(ring + stage * C::kStage);
       const int c = lane % kChunks;
 #pragma unroll
       for (int j = 0; j < kMmaKeys / kPerCopy; ++j) {
@@ -211,7 +206,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
       cp_async_wait<kStages - 2>();
       __syncwarp();
       unsigned char* kt = ring + stage * C::kStage;
-      const uint32_t ka = s_addr(kt), va = ka + C::kPlane;
+      const uint32_t ka = smem_u32(kt), va = ka + C::kPlane;
       bad |= (bad_stages >> stage) & 1u;
       // scores
       float z[MT][2][4];

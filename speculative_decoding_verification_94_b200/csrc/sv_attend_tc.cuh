@@ -1,0 +1,674 @@
+// sv_attend_tc.cuh -- bf16 attention of many rows (long drafts, candidate
+// trees) on the fifth-generation tensor cores.
+//
+// Products.  A tile is 128 keys.  S = Q K^T is one 128 x 128 product (128
+// lanes of tensor memory), O += P V one of 128 x D; their operands come from
+// shared memory (TMA, 128-byte swizzle), the weights P from tensor memory.
+// The lanes are the rows of a row tile of RT = 32, 64 or 128; with fewer than
+// 128 rows they are repeated, and copy c of a row takes the weights of the
+// c-th part of the keys only (the others are zero), so that all four warps
+// of a warp group work on the softmax of every tile; the copies add up at the
+// end.  The products take the same time whatever RT is, 0.5 us of the 1.5 us
+// in which one SM's share of HBM brings the 64 KB of a tile.
+//
+// Roles.  One warp issues the copies, one the products.  Two warp groups take
+// the even and the odd tiles, each with its own S, P, O, maximum and sum, so
+// that one's softmax runs under the other's products, and neither waits for
+// the other.  O stays in tensor memory; it is rescaled only when the maximum
+// grows by more than 2^8 (a weight may then be up to 2^8, which costs no
+// precision: the sum is fp32).  P is stored over S, as the sum of two
+// bf16 (in two products): with one, the output's error grew beyond its own
+// rounding.
+//
+// Every wait has a time limit; a block whose wait runs out gives NaN for its
+// segments, sets SV_DEV_TIMEOUT and goes on to the end.
+#pragma once
+
+#include <cuda.h>
+
+#include "sv_attend.cuh"
+#include "sv_attend_mma.cuh"
+#include "sv_device.cuh"
+
+namespace sv {
+
+constexpr int kTcU = 128;            // keys of a tile
+constexpr int kTcSoftmax = 256;      // threads of the two warp groups
+constexpr int kTcThreads = 320;      // + copy warp + product warp
+constexpr int kTcStages = 3;
+
+template <int D>
+struct TcCfg {
+  static constexpr int kTile = kTcU * D * 2;               // bytes of keys (or values)
+  static constexpr int kHalf = kTcU * 128;                 // 64 columns of a tile: 128-byte rows
+  static constexpr int kOffK = kTcU * D * 2;               // after Q
+  static constexpr int kOffV = kOffK + kTcStages * kTile;
+  static constexpr int kOffEnd = kOffV + kTcStages * kTile;
+  static constexpr int kOffMl = kOffEnd;                   // [2][128] (m, l)
+  static constexpr int kOffBar = kOffMl + 2048;
+  static constexpr int kOffMisc = kOffBar + 256;
+  static constexpr int kOffShare = kOffMisc + 64;
+  static constexpr int kSmem = kOffShare + kShareBytes;
+  // output columns added at a time, through the space of Q
+  static constexpr int kCols = D == 128 ? 32 : 16;
+};
+
+// ---------------------------------------------------------------------------
+// PTX of the tensor cores and the tensor maps.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// D = A B (+ D): A and B in shared memory.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          bool add) {
+  asm volatile(
+      "{\n\t.reg .pred P;\n\tsetp.ne.u32 P, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, P;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// A in tensor memory.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          bool add) {
+  asm volatile(
+      "{\n\t.reg .pred P;\n\tsetp.ne.u32 P, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, P;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(a)
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// A box of the cache: 64 columns x box rows of one page and head.
+__device__ __forceinline__ void tma_page(void* dst, const CUtensorMap* map, int col, int token,
+                                         int head, int page, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(col), "r"(token), "r"(head), "r"(page)
+      : "memory");
+}
+// Named barrier of the softmax threads.
+__device__ __forceinline__ void softmax_sync() {
+  asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+
+// Shared-memory operand with 128-byte swizzle: 8 rows of 128 bytes are one
+// 1024-byte atom; `lead` is the distance of 64-element blocks along the
+// contiguous dimension where that dimension is not the summed one.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// bf16 x bf16 -> fp32, M = 128; b_cols: B is contiguous along N.
+__host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_cols) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_cols ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+struct TcParams {
+  AttendParams a;
+  int box;  // rows of a copy box: keys of a page within a tile
+};
+
+template <int D, int RT>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attend_tc_kernel(const TcParams tp, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap) {
+  using C = TcCfg<D>;
+  constexpr int kCopies = 128 / RT;          // copies of a row among the lanes
+  constexpr int kKeys = kTcU / kCopies;      // keys of a copy
+  constexpr int kPart = att_partial_floats(RT, D);
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const AttendParams& p = tp.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned char* s_q = smem;
+  float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t *k_full = bars, *k_empty = bars + 3, *v_full = bars + 6, *v_empty = bars + 9,
+           *s_full = bars + 12, *p_ready = bars + 14, *pv_done = bars + 16, *q_full = bars + 18;
+  int* misc = reinterpret_cast<int*>(smem + C::kOffMisc);
+  volatile int* s_abort = misc;      // a wait ran out
+  int* s_bad = misc + 1;             // the segment's keys are on a bad page
+  int* s_fix = misc + 2;             // a new token's value is not finite
+  int* s_flag = misc + 3;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc + 4);
+
+  if (tid == 0) {
+    for (int i = 0; i < kTcStages; ++i) {
+      mbar_init(k_full + i, 1);
+      mbar_init(k_empty + i, 1);
+      mbar_init(v_full + i, 1);
+      mbar_init(v_empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(p_ready + i, 128);
+      mbar_init(pv_done + i, 1);
+    }
+    mbar_init(q_full, kTcSoftmax);
+    fence_mbar_init();
+    misc[0] = misc[1] = misc[2] = 0;
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(s_tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  AttCursor<kTcU, RT> cur;
+  const AttShare s = att_share<kTcU, RT, kTcThreads>(p, cur, smem + C::kOffShare);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  if (warp == 8) {
+    // ------------------------------ copies --------------------------------
+    const int boxes = kTcU / tp.box;              // <= 16 per 64 columns
+    constexpr int kHalves = D / 64;
+    const int bi = lane & 15, half = lane >> 4;
+    const bool mine = bi < boxes && half < kHalves;
+    long long u = s.u0;
+    auto page_of = [&]() {  // out of the pool: zeros are copied
+      const int pos = cur.tile * kTcU + bi * tp.box;
+      if (u >= s.u1 || !mine || pos >= cur.kv + cur.q) return p.num_pages;
+      const int id = __ldg(p.table + (long long)cur.b * p.max_pages + pos / p.page);
+      return id >= 0 && id < p.num_pages ? id : p.num_pages;
+    };
+    int page = page_of();
+    int slot = 0, round = 0;
+    bool ok = true;
+    for (; u < s.u1 && ok;) {
+      const int h = cur.seg / cur.mt;
+      const int token = (cur.tile * kTcU + bi * tp.box) % p.page;
+      const uint32_t off = half * C::kHalf + bi * tp.box * 128;
+      const int id = page;
+      ++u;
+      cur.advance(p);
+      page = page_of();
+      for (int kvs = 0; kvs < 2; ++kvs) {
+        uint64_t* full = (kvs ? v_full : k_full) + slot;
+        uint64_t* empty = (kvs ? v_empty : k_empty) + slot;
+        if (round) ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty, (round - 1) & 1));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(full, C::kTile);
+        __syncwarp();
+        if (mine) {
+          if (kvs == 0)
+            tma_page(smem + C::kOffK + slot * C::kTile + off, &kmap, half * 64, token, h, id, full);
+          else
+            tma_page(smem + C::kOffV + slot * C::kTile + off, &vmap, half * 64, token, h, id, full);
+        }
+      }
+      if (++slot == kTcStages) slot = 0, ++round;
+    }
+    if (!ok) {  // the copies under way end before the block does
+      *s_abort = 1;
+      kv_flag(p.status, SV_DEV_TIMEOUT);
+      for (int i = 0; i < kTcStages; ++i) {
+        mbar_wait_bounded(k_full + i, (round - (i >= slot)) & 1);
+        mbar_wait_bounded(v_full + i, (round - (i >= slot)) & 1);
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------ products ------------------------------
+    if (lane == 0) {
+      constexpr uint32_t kIdQk = tc_idesc(kTcU, false), kIdPv = tc_idesc(D, true);
+      const uint32_t qa = smem_u32(s_q);
+      int kg = 0, vg = 0;      // tiles whose keys, values have been used
+      int streams[2] = {0, 0};  // tiles of each warp group
+      int segs = 0;
+      bool ok = true;
+      auto qk = [&](int w) {
+        const int slot = kg % kTcStages;
+        ok = ok && mbar_wait_bounded(k_full + slot, (kg / kTcStages) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t ka = smem_u32(smem + C::kOffK + slot * C::kTile);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t o = (ks / 4) * C::kHalf + (ks % 4) * 32;
+          tc_mma_ss(tmem + w * 128, tc_desc(qa + o, 16), tc_desc(ka + o, 16), kIdQk, ks > 0);
+        }
+        tc_commit(s_full + w);
+        tc_commit(k_empty + slot);
+        ++kg;
+      };
+      for (long long u = s.u0; u < s.u1 && ok;) {
+        const int left = cur.tiles - cur.tile;
+        const int cnt = s.u1 - u < left ? (int)(s.u1 - u) : left;
+        ok = mbar_wait_bounded(q_full, segs & 1);
+        ++segs;
+        if (!ok) break;
+        qk(0);
+        if (cnt > 1) qk(1);
+        for (int k = 0; k < cnt && ok; ++k) {
+          const int w = k & 1;
+          ok = mbar_wait_bounded(p_ready + w, streams[w] & 1);
+          ++streams[w];
+          const int slot = vg % kTcStages;
+          ok = ok && mbar_wait_bounded(v_full + slot, (vg / kTcStages) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t va = smem_u32(smem + C::kOffV + slot * C::kTile);
+          const uint32_t pa = tmem + w * 128, o = tmem + 256 + w * 128;
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int ks = 0; ks < kTcU / 16; ++ks)
+              tc_mma_ts(o, pa + (ks / 2) * 32 + part * 16 + (ks & 1) * 8,
+                        tc_desc(va + ks * 2048, C::kHalf), kIdPv, k >= 2 || part || ks);
+          tc_commit(pv_done + w);
+          tc_commit(v_empty + slot);
+          ++vg;
+          if (k + 2 < cnt) qk(w);
+        }
+        u += cnt;
+        if (cnt == left)
+          cur.next_segment(p);
+        else
+          cur.tile += cnt;
+      }
+      if (!ok) {
+        *s_abort = 1;
+        kv_flag(p.status, SV_DEV_TIMEOUT);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------- softmax -------------------------------
+    const int w = warp >> 2, quad = warp & 3;
+    const int lr = quad * 32 + lane;              // lane of tensor memory
+    const int row = lr % RT, copy = lr / RT;      // copy is the same for a warp
+    const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
+    const uint32_t s_at = tmem + lane_at + w * 128, o_at = tmem + lane_at + 256 + w * 128;
+    int tiles_done = 0;                           // of this warp group
+    int tile_g = 0;                               // of the block
+    bool dead = false;
+    for (long long u = s.u0; u < s.u1;) {
+      const int h = cur.seg / cur.mt, row0 = (cur.seg % cur.mt) * RT;
+      const int rows = min(RT, cur.q * p.g - row0);
+      const int tile0 = cur.tile, left = cur.tiles - cur.tile;
+      const int cnt = s.u1 - u < left ? (int)(s.u1 - u) : left;
+      const int kv = cur.kv, len = cur.kv + cur.q;
+      const int32_t* par = p.parents ? p.parents + (long long)cur.b * p.n : nullptr;
+      const int32_t* trow = p.table + (long long)cur.b * p.max_pages;
+      // the rows of q, and whether all pages are in the pool
+      {
+        const int r = tid & 127, hf = tid >> 7;
+        const int qr = row0 + r % RT;
+        const bool on = r % RT < rows;
+        const int i = on ? qr / p.g : 0, gi = on ? qr - i * p.g : 0;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(p.q) + cur.b * p.q_b + i * p.q_t +
+            (long long)(h * p.g + gi) * D) + hf * (D / 16);
+        constexpr int kPer = D / 16;  // 16-byte pieces of half a row
+        uint4 x[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) x[j] = on ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int c = hf * kPer + j;
+          *reinterpret_cast<uint4*>(s_q + (c / 8) * C::kHalf + r * 128 +
+                                    (((c % 8) ^ (r & 7)) << 4)) = x[j];
+        }
+        const int first = (int)((long long)tile0 * kTcU / p.page);
+        const int last = (int)((min((long long)(tile0 + cnt) * kTcU, (long long)len) - 1) / p.page);
+        for (int j = first + tid; j <= last; j += kTcSoftmax) {
+          const int id = __ldg(trow + j);
+          if (id < 0 || id >= p.num_pages) *s_bad = 1;
+        }
+      }
+      fence_async_smem();
+      tc_fence_before();
+      mbar_arrive(q_full);
+      const int qi = min((row0 + row) / p.g, cur.q - 1);
+      float m = -INFINITY, l = 0.f;
+      bool tree_ok = true;
+      for (int k = w; k < cnt; k += 2) {
+        if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_bounded(s_full + w, tiles_done & 1));
+        if (dead) {
+          *s_abort = 1;
+          break;
+        }
+        tc_fence_after();
+        const int pos0 = (tile0 + k) * kTcU + copy * kKeys;
+        // S is read twice, 32 columns at a time, for the maximum and for the
+        // weights: tensor memory is near, registers are not plenty.
+        const uint32_t mine = s_at + copy * kKeys;
+        const bool tail = (tile0 + k + 1) * kTcU > kv;
+        uint32_t seen[kKeys / 32];
+        if (tail) {
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; ++c)
+            seen[c] = pos0 + c * 32 + 32 > kv
+                          ? att_tail_bits<32>(par, qi, pos0 + c * 32, kv, tree_ok)
+                          : 0xffffffffu;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kKeys / 32; ++c) {
+          uint32_t x[32];
+          tc_ld32(mine + c * 32, x);
+          tc_wait_ld();
+          if (tail) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(seen[c] >> e & 1u)) x[e] = 0xff800000u;
+          }
+          float t2[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 32; ++e) t2[e & 3] = fmaxf(t2[e & 3], __uint_as_float(x[e]));
+          top = fmaxf(fmaxf(t2[0], t2[1]), fmaxf(t2[2], t2[3]));
+        }
+        top *= p.scale_log2;  // scale > 0 here
+        // a new maximum only when weights would pass 2^8
+        const bool grow = top > m + 8.f || (m == -INFINITY && top != -INFINITY);
+        if (__any_sync(0xffffffffu, grow) && k >= 2) {
+          dead = !__all_sync(0xffffffffu, mbar_wait_bounded(pv_done + w, (tiles_done - 1) & 1));
+          if (dead) {
+            *s_abort = 1;
+            break;
+          }
+          tc_fence_after();
+          const float a = grow ? pow2(m - top) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t y[32];
+            tc_ld32(o_at + c, y);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * a);
+            tc_st32(o_at + c, y);
+          }
+        }
+        if (grow) {
+          l *= pow2(m - top);
+          m = top;
+        }
+        const float ms = m == -INFINITY ? 0.f : m;
+        const unsigned long long cc = f2_pack(p.scale_log2, p.scale_log2), mm = f2_pack(-ms, -ms);
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        // P over S: the 32 columns of 32 keys take their bf16 pairs, first
+        // the first parts (16 columns), then the rests
+#pragma unroll
+        for (int c = 0; c < kKeys / 32; ++c) {
+          uint32_t x[32];
+          tc_ld32(mine + c * 32, x);
+          tc_wait_ld();
+          if (tail) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(seen[c] >> e & 1u)) x[e] = 0xff800000u;
+          }
+          uint32_t y[32];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float a, b;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), cc,
+                             mm),
+                      a, b);
+            a = pow2(a);
+            b = pow2(b);
+            sum[e & 1] += a;
+            sum[2 + (e & 1)] += b;
+            y[e] = pack_bf16(a, b);
+            y[16 + e] = pack_bf16(a - bf16_lo(y[e]), b - bf16_hi(y[e]));
+          }
+          tc_st32(mine + c * 32, y);
+        }
+        if constexpr (kCopies > 1) {  // the other copies' keys
+          const uint32_t zero[32] = {};
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c / (kKeys / 32) != copy) tc_st32(s_at + c * 32, zero);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (tail) {
+          // Values past the end become zeros, and so do new tokens' values
+          // that are not finite: as 0 x inf they would reach rows that do not
+          // see them; they are added to those that do at the end.
+          const int g = tile_g + k, slot = g % kTcStages;
+          dead = !__all_sync(0xffffffffu,
+                             mbar_wait_bounded(v_full + slot, (g / kTcStages) & 1));
+          if (dead) {
+            *s_abort = 1;
+            break;
+          }
+          const int pos = (tile0 + k) * kTcU + lr;
+          if (pos >= kv && (pos >= len || cur.q > 1)) {
+            unsigned char* vrow = smem + C::kOffV + slot * C::kTile + lr * 128;
+#pragma unroll 1
+            for (int c = 0; c < D / 8; ++c) {
+              uint4* at = reinterpret_cast<uint4*>(vrow + (c / 8) * C::kHalf + (c % 8) * 16);
+              uint32_t y[4] = {0, 0, 0, 0};
+              if (pos < len) {
+                const uint4 v = *at;
+                y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+                bool any = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  any |= bf16x2_not_finite(y[e]);
+                  if ((y[e] & 0x7f80u) == 0x7f80u) y[e] &= 0xffff0000u;
+                  if ((y[e] & 0x7f800000u) == 0x7f800000u) y[e] &= 0xffffu;
+                }
+                if (!any) continue;
+                *s_fix = 1;
+              }
+              *at = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          }
+          fence_async_smem();
+        }
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_ready + w);
+        ++tiles_done;
+      }
+      const bool used = w < cnt;
+      if (used && !dead) {
+        dead = !__all_sync(0xffffffffu, mbar_wait_bounded(pv_done + w, (tiles_done - 1) & 1));
+        if (dead) *s_abort = 1;
+      }
+      tc_fence_after();
+      tile_g += cnt;
+      // ---- the row's parts together --------------------------------------------
+      if (!tree_ok) {
+        l = __int_as_float(0x7fc00000);
+        if (row < rows) kv_flag(p.status, SV_DEV_BAD_TREE);
+      }
+      s_ml[w * 128 + lr] = make_float2(m, l);
+      softmax_sync();
+      const bool gone = __any_sync(0xffffffffu, *s_abort != 0);
+      const bool bad = *s_bad != 0, fix = *s_fix != 0;
+      if (gone) dead = true;
+      if (bad && tid == 0) kv_flag(p.status, SV_DEV_BAD_INDEX);
+      auto row_stats = [&](int r, float& top, float& sum) {
+        top = -INFINITY;
+        sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2 * kCopies; ++j)
+          top = fmaxf(top, s_ml[(j / kCopies) * 128 + (j % kCopies) * RT + r].x);
+#pragma unroll
+        for (int j = 0; j < 2 * kCopies; ++j) {
+          const float2 ml = s_ml[(j / kCopies) * 128 + (j % kCopies) * RT + r];
+          sum += top == -INFINITY ? ml.y : pow2(ml.x - top) * ml.y;
+        }
+        if (bad || gone) sum = __int_as_float(0x7fc00000);
+      };
+      float top, sum;
+      row_stats(row, top, sum);
+      const float f = top == -INFINITY ? 0.f : pow2(m - top);
+      const bool whole = tile0 == 0 && cnt == cur.tiles;
+      float* part = p.partial + ((long long)blockIdx.x * 2 + (tile0 == 0 ? 1 : 0)) * kPart;
+      float* stage = reinterpret_cast<float*>(s_q);  // [2][128][kCols]
+      constexpr int kPieces = C::kCols / 4;
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += C::kCols) {
+        float4* dst = reinterpret_cast<float4*>(stage + (w * 128 + lr) * C::kCols);
+        if (used && !gone) {
+          if constexpr (C::kCols == 32) {
+            uint32_t y[32];
+            tc_ld32(o_at + c0, y);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j)
+              dst[j ^ (lr & (kPieces - 1))] = make_float4(
+                  __uint_as_float(y[4 * j]) * f, __uint_as_float(y[4 * j + 1]) * f,
+                  __uint_as_float(y[4 * j + 2]) * f, __uint_as_float(y[4 * j + 3]) * f);
+          } else {
+            uint32_t y[32];
+            tc_ld32(o_at + (c0 & ~31), y);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+              float z[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                z[e] = __uint_as_float(c0 & 16 ? y[16 + 4 * j + e] : y[4 * j + e]) * f;
+              dst[j ^ (lr & (kPieces - 1))] = make_float4(z[0], z[1], z[2], z[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kPieces; ++j) dst[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        softmax_sync();
+        for (int it = tid; it < rows * kPieces; it += kTcSoftmax) {
+          const int r = it / kPieces, j = it % kPieces;
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int q = 0; q < 2 * kCopies; ++q) {
+            const int at = (q / kCopies) * 128 + (q % kCopies) * RT + r;
+            const float4 b = reinterpret_cast<const float4*>(
+                stage + at * C::kCols)[j ^ (at & (kPieces - 1))];
+            a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+          }
+          const int col = c0 + j * 4;
+          if (fix) {
+            float* av = &a.x;
+            const int i = (row0 + r) / p.g;
+            for (int t = max(0, tile0 * kTcU - kv); t < cur.q; ++t) {
+              const int pos = kv + t;
+              if (pos >= (tile0 + cnt) * kTcU) break;
+              int up = i;
+              if (par)
+                while (up > t) up = par[up];
+              else
+                up = t <= i ? t : -1;
+              if (up != t) continue;
+              const int pi = pos / p.page, id = trow[pi];
+              if (id < 0 || id >= p.num_pages) continue;
+              const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + id * p.c_page +
+                                       (long long)(pos - pi * p.page) * p.c_token + h * p.c_head +
+                                       col;
+              for (int e = 0; e < 4; ++e) {
+                const float y = __bfloat162float(v[e]);
+                if (not_finite(y)) av[e] += y;
+              }
+            }
+          }
+          if (whole) {
+            float rt, rs;
+            row_stats(r, rt, rs);
+            const float inv = 1.f / rs;
+            uint2 y;
+            y.x = pack_bf16(a.x * inv, a.y * inv);
+            y.y = pack_bf16(a.z * inv, a.w * inv);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) +
+                                      att_out_row(p, cur.b, h, row0 + r) * D + col) = y;
+          } else {
+            __stcg(reinterpret_cast<float4*>(part + r * D + col), a);
+          }
+        }
+        softmax_sync();
+      }
+      if (w == 0 && lr < rows) {
+        if (whole) {
+          if (p.lse) p.lse[att_out_row(p, cur.b, h, row0 + lr)] = (top + log2f(sum)) * kLn2;
+        } else {
+          __stcg(part + RT * D + lr, top);
+          __stcg(part + RT * D + RT + lr, sum);
+        }
+      }
+      if (!whole) {
+        const long long seg_u0 = u - tile0, seg_u1 = seg_u0 + cur.tiles;
+        const int c0 = s.block_of(seg_u0), c1 = s.block_of(seg_u1 - 1);
+        __threadfence();
+        softmax_sync();
+        if (tid == 0) {
+          const uint32_t before = atomicAdd(p.counters + c0, 1u);
+          *s_flag = before == (uint32_t)(c1 - c0);
+          if (*s_flag) {
+            p.counters[c0] = 0;
+            __threadfence();
+          }
+        }
+        softmax_sync();
+        if (*s_flag)
+          att_join<__nv_bfloat16, D, RT, kTcSoftmax>(p, cur.b, h, row0, rows, c0, c1);
+      }
+      tc_fence_before();
+      if (tid == 0) *s_bad = *s_fix = 0;
+      softmax_sync();  // before the next segment's q and flags
+      u += cnt;
+      if (tile0 + cnt == cur.tiles)
+        cur.next_segment(p);
+      else
+        cur.tile += cnt;
+    }
+    if (dead && lane == 0) kv_flag(p.status, SV_DEV_TIMEOUT);
+  }
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+  att_fill_padding<__nv_bfloat16, kTcThreads>(p);
+}
+
+}  // namespace sv

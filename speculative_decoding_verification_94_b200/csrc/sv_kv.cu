@@ -7,6 +7,7 @@
 
 #include "sv_attend.cuh"
 #include "sv_attend_mma.cuh"
+#include "sv_attend_tc.cuh"
 #include "sv_kv_pages.cuh"
 
 namespace sv {
@@ -69,11 +70,17 @@ int padded_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
 constexpr size_t kCounterBytes = (4 * kAttMaxBlocks + 255) / 256 * 256;
 
-// Enough for either kernel: 32 rows at most, 16 in the general one.
-size_t attend_ws(int head_dim, sv_dtype dt) {
-  const int rows = dt == SV_BF16 && (head_dim == 64 || head_dim == 128) ? 32 : kGenR;
-  return kCounterBytes +
-         (size_t)kAttMaxBlocks * 2 * att_partial_floats(rows, padded_dim(head_dim)) * 4;
+// Rows of a row tile, which set the size of a partial result.  16 also covers
+// the general kernel, which any bf16 call may need for its strides.
+int tile_rows(int rows, int head_dim, sv_dtype dt) {
+  if (dt != SV_BF16 || (head_dim != 64 && head_dim != 128) || rows <= 16) return 16;
+  return rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+}
+
+size_t attend_ws(int rows, int head_dim, sv_dtype dt) {
+  return kCounterBytes + (size_t)kAttMaxBlocks * 2 *
+                             att_partial_floats(tile_rows(rows, head_dim, dt), padded_dim(head_dim)) *
+                             4;
 }
 
 template <class K>
@@ -101,6 +108,70 @@ cudaError_t launch_general(AttendParams& p, cudaStream_t s) {
       return launch_attend(attend_general_kernel<T, 256, VEC>, p, kGenThreads, sizeof(GenSmem<256>),
                            s);
   }
+}
+
+// ---------------------------------------------------------------------------
+// The tensor-memory kernel: tensor maps over the cache
+// ---------------------------------------------------------------------------
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+// Copies take up to 16 boxes of whole pages, or of 128 rows of a page.
+int tc_box(int page) {
+  if (page >= kTcU) return page % kTcU == 0 ? kTcU : 0;
+  return page >= 8 && kTcU % page == 0 ? page : 0;
+}
+
+bool tc_map(const AttendParams& p, const void* base, int box, CUtensorMap* map) {
+  const EncodeTiled enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.page, (cuuint64_t)p.hkv,
+                              (cuuint64_t)p.num_pages};
+  // a dimension of one has no stride of its own
+  const cuuint64_t strides[3] = {
+      (cuuint64_t)(p.page > 1 ? p.c_token : p.d) * 2, (cuuint64_t)(p.hkv > 1 ? p.c_head : p.d) * 2,
+      (cuuint64_t)(p.num_pages > 1 ? p.c_page : p.d) * 2};
+  for (cuuint64_t x : strides)
+    if (x >= (1ull << 40)) return false;
+  const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
+             boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int RT>
+cudaError_t launch_tc(const TcParams& tp, const CUtensorMap& km, const CUtensorMap& vm,
+                      cudaStream_t s) {
+  auto kernel = attend_tc_kernel<D, RT>;
+  cudaError_t e =
+      ensure_kernel_attrs(reinterpret_cast<const void*>(kernel), TcCfg<D>::kSmem, false);
+  if (e != cudaSuccess) return e;
+  int sms = 0;
+  if ((e = sm_count(&sms)) != cudaSuccess) return e;
+  if ((e = launch_mark_before(s)) != cudaSuccess) return e;
+  kernel<<<(unsigned)std::min(sms, kAttMaxBlocks), kTcThreads, TcCfg<D>::kSmem, s>>>(tp, km, vm);
+  return launch_mark_after(s, cudaGetLastError());
+}
+
+template <int D>
+cudaError_t launch_tc(const TcParams& tp, const CUtensorMap& km, const CUtensorMap& vm,
+                      cudaStream_t s) {
+  const int rows = tp.a.n * tp.a.g;
+  if (rows <= 32) return launch_tc<D, 32>(tp, km, vm, s);
+  if (rows <= 64) return launch_tc<D, 64>(tp, km, vm, s);
+  return launch_tc<D, 128>(tp, km, vm, s);
 }
 
 template <int D>
@@ -215,7 +286,8 @@ size_t sv_kv_attend_workspace_size(int B, int n, int q_heads, int heads, int hea
   if (B < 0 || n < 1 || heads < 1 || q_heads < 1 || head_dim < 1 || head_dim > 256 ||
       (dtype != SV_F32 && dtype != SV_BF16))
     return 0;
-  return attend_ws(head_dim, dtype);
+  if (n > 1024 || q_heads % heads) return 0;
+  return attend_ws(n * (q_heads / heads), head_dim, dtype);
 }
 
 sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_stride,
@@ -239,7 +311,9 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_st
       !aligned_or_null(device_status, 4))
     return SV_ERR_INVALID_ARG;
   if (q_heads > (1 << 16) || (long long)B * n > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
-  if (!workspace || !aligned(workspace, 16) || workspace_bytes < attend_ws(cache->head_dim, cache->dtype))
+  if (!workspace || !aligned(workspace, 16) ||
+      workspace_bytes <
+          attend_ws(n * (q_heads / cache->heads), cache->head_dim, cache->dtype))
     return SV_ERR_WORKSPACE;
   AttendParams p = {};
   p.q = q;
@@ -275,7 +349,15 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_st
   const bool pairs = common_width({addr(q), p.q_b * es, p.q_t * es}) >= 4 &&
                      aligned(out, 16);
   cudaError_t e;
-  if (cache->dtype == SV_BF16 && vec && pairs && p.d == 128)
+  const int box = tc_box(p.page);
+  CUtensorMap km, vm;
+  if (cache->dtype == SV_BF16 && vec && aligned(out, 16) && (p.d == 64 || p.d == 128) &&
+      p.n * p.g > 16 && box && scale > 0.f &&
+      common_width({addr(q), p.q_b * es, p.q_t * es}) == 16 && tc_map(p, p.k, box, &km) &&
+      tc_map(p, p.v, box, &vm)) {
+    const TcParams tp = {p, box};
+    e = p.d == 128 ? launch_tc<128>(tp, km, vm, s) : launch_tc<64>(tp, km, vm, s);
+  } else if (cache->dtype == SV_BF16 && vec && pairs && p.d == 128)
     e = launch_mma<128>(p, s);
   else if (cache->dtype == SV_BF16 && vec && pairs && p.d == 64)
     e = launch_mma<64>(p, s);
