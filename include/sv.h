@@ -324,7 +324,7 @@ SV_API sv_status sv_verify_tree_sample(const void* target_logits, sv_dtype t_dty
  */
 SV_API sv_status sv_extract_topk_kd(const void* logits, sv_dtype dt, int rows, int V, int K,
                                     float temperature, float* topk_logp, int32_t* topk_idx,
-                                    float* lse, void* workspace, size_t workspace_bytes,
+                                    float* lse, void* scratch, size_t scratch_bytes,
                                     int32_t* device_status, void* stream);
 
 /*
@@ -484,18 +484,22 @@ SV_API sv_status sv_kv_append(const sv_kv_cache* cache, const void* k, const voi
  *   are on a page outside [0, num_pages) SV_DEV_BAD_INDEX, a row with a bad
  *   parent on its way up SV_DEV_BAD_TREE; their outputs are NaN (with
  *   BAD_TREE and BAD_INDEX, rows of the same request that share a tile may be NaN too).
- *   workspace: sv_kv_attend_workspace_size(...) bytes.
- * Sums and softmax statistics are fp32.  The split of a sequence over the
+ *   scratch: sv_kv_attend_scratch_size(...) bytes of device memory, 16-byte
+ *   aligned, used by this call alone.  Unlike the workspaces above it may hold
+ *   anything before the call and holds anything after it, so a buffer that is
+ *   to serve as their workspace has to be zeroed again.
+ * Two launches: the attention, and the join of sequences that several blocks
+ * shared.  Sums and softmax statistics are fp32.  The split of a sequence over the
  * device's blocks depends on all lengths of the batch, so a request's last
  * bits can differ between batches; a repeated call gives the same bits.
  */
-SV_API size_t sv_kv_attend_workspace_size(int B, int n, int q_heads, int heads, int head_dim,
-                                          sv_dtype dtype);
+SV_API size_t sv_kv_attend_scratch_size(int B, int n, int q_heads, int heads, int head_dim,
+                                        sv_dtype dtype);
 SV_API sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_stride,
                               int64_t token_stride, int B, int n, int q_heads,
                               const int32_t* block_table, int max_pages, const int32_t* kv_len,
                               const int32_t* q_len, const int32_t* parents, float scale, void* out,
-                              float* lse, void* workspace, size_t workspace_bytes,
+                              float* lse, void* scratch, size_t scratch_bytes,
                               int32_t* device_status, void* stream);
 
 /*

@@ -19,8 +19,10 @@
 // of all requests in order are cut into as many equal runs as there are
 // blocks.  A block therefore holds at most two segments that it shares with
 // other blocks, its first and its last; their partial results (output, m, l)
-// go to the workspace, and the last block to arrive at a shared segment joins
-// its parts in block order, so results do not depend on the timing.
+// go to the scratch buffer, and a second launch joins them in block order.  (The
+// last block to finish a segment joined them at first: 128 rows of a few
+// parts, or 40 rows of 19, are 0.4 MB to read and clear, 10 to 27 us on one
+// SM and 3 us over all of them.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -34,6 +36,11 @@
 
 namespace sv {
 
+// A segment that starts in a block and ends in block c1 (c1 < 0: none).
+struct AttShared {
+  int b, h, row0, rows, c1, pad[3];
+};
+
 struct AttendParams {
   const void* q;
   const void *k, *v;
@@ -44,8 +51,8 @@ struct AttendParams {
   long long q_b, q_t;                 // strides of q, elements
   long long c_page, c_token, c_head;  // strides of the cache, elements
   float scale_log2;
-  uint32_t* counters;  // [grid] arrivals at the segment that starts in block i
-  float* partial;      // [grid][2] partial results
+  AttShared* shared;  // [grid] the shared segment that starts in block i
+  float* partial;            // [grid][2] partial results
   int32_t* status;
 };
 
@@ -220,103 +227,152 @@ __device__ __forceinline__ long long att_out_row(const AttendParams& p, int b, i
 
 // Tokens that no row was computed for: zeros and lse -inf for those behind a
 // request's own, NaN for a failed request.
-template <class T, int THREADS>
-__device__ __forceinline__ void att_fill_padding(const AttendParams& p) {
-  const int hq = p.hkv * p.g;
+// Warps [w0, w0 + warps) of every block take part.
+template <class T>
+__device__ __forceinline__ void att_fill_padding(const AttendParams& p, int w0, int warps) {
+  const int hq = p.hkv * p.g, lane = threadIdx.x & 31;
   const long long tokens = (long long)p.B * p.n;
-  for (long long t = blockIdx.x; t < tokens; t += gridDim.x) {
-    const int b = (int)(t / p.n), i = (int)(t - (long long)b * p.n);
-    int kv, q;
-    const bool ok = att_lens(p, b, kv, q);
-    if (ok && i < q) continue;
-    const float nan = __int_as_float(0x7fc00000);
-    if (!ok && i == 0 && threadIdx.x == 0) kv_flag(p.status, SV_DEV_BAD_LEN);
-    const T z = from_f32<T>(ok ? 0.f : nan);
-    T* o = static_cast<T*>(p.out) + t * hq * p.d;
-    for (int e = threadIdx.x; e < hq * p.d; e += THREADS) o[e] = z;
-    if (p.lse)
-      for (int e = threadIdx.x; e < hq; e += THREADS) p.lse[t * hq + e] = ok ? -INFINITY : nan;
+  const long long step = (long long)gridDim.x * warps;
+  const long long mine = (long long)blockIdx.x * warps + (threadIdx.x >> 5) - w0;
+  // a lane looks at a token, the warp fills those that need it
+  for (long long t0 = mine; t0 < tokens; t0 += 32 * step) {
+    const long long t = t0 + lane * step;
+    int what = 0;
+    if (t < tokens) {
+      const int b = (int)(t / p.n), i = (int)(t - (long long)b * p.n);
+      int kv, q;
+      if (!att_lens(p, b, kv, q)) {
+        what = 2;
+        if (i == 0) kv_flag(p.status, SV_DEV_BAD_LEN);
+      } else if (i >= q) {
+        what = 1;
+      }
+    }
+    for (uint32_t left = __ballot_sync(0xffffffffu, what != 0); left; left &= left - 1) {
+      const int j = __ffs(left) - 1;
+      const bool bad = __shfl_sync(0xffffffffu, what, j) == 2;
+      const long long at = (t0 + j * step) * hq;
+      const float nan = __int_as_float(0x7fc00000);
+      const T z = from_f32<T>(bad ? nan : 0.f);
+      T* o = static_cast<T*>(p.out) + at * p.d;
+      for (int e = lane; e < hq * p.d; e += 32) o[e] = z;
+      if (p.lse)
+        for (int e = lane; e < hq; e += 32) p.lse[at + e] = bad ? nan : -INFINITY;
+    }
   }
 }
 
-// Joins the parts of a shared segment.  A warp takes a row; its lanes hold
-// the parts' weights (32 parts at a time) and then the row's DP values.  The
-// parts are set back to zero as they are read.
-template <class T, int DP, int RT, int THREADS>
-__device__ __forceinline__ void att_join(const AttendParams& p, int b, int h, int row0, int rows,
-                                         int c0, int c1) {
-  constexpr int VPL = DP / 32;
-  constexpr int kStride = att_partial_floats(RT, DP);
+// The place of a block's part of a segment it shares; the block in which the
+// segment starts keeps it in its second place and notes the segment.
+template <int DP, int RT>
+__device__ __forceinline__ float* att_part(const AttendParams& p, int block, bool starts) {
+  return p.partial + ((long long)block * 2 + starts) * att_partial_floats(RT, DP);
+}
+__device__ __forceinline__ void att_note(const AttendParams& p, const AttShare& s, int b, int h,
+                                         int row0, int rows, long long seg_u1) {
+  p.shared[blockIdx.x] = AttShared{b, h, row0, rows, s.block_of(seg_u1 - 1), {0, 0, 0}};
+}
+// Before any note, by one thread of every block.
+__device__ __forceinline__ void att_clear_note(const AttendParams& p) {
+  p.shared[blockIdx.x].c1 = -1;
+}
+
+// Joins the parts of shared segments: block x takes the segment that starts
+// in block x of the first launch.  kSplit warps share a row's parts; lanes
+// hold the parts' weights, then the row's values, eight parts in flight.
+constexpr int kJoinThreads = 128;
+template <class T, int DP, int RT>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendParams p) {
+  constexpr int kSplit = RT >= 128 ? 1 : RT == 64 ? 2 : 4;
+  constexpr int kRowsHere = 4 / kSplit;
+  constexpr int kV = DP / 32;  // values of a lane
+  constexpr int kBatch = 8;
+  __shared__ float s_m[4], s_l[4], s_o[4][DP];
+  pdl_wait();
+  const AttShared g = p.shared[blockIdx.x];
+  if (g.c1 < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int parts = c1 - c0 + 1;
-  // a block keeps the part of a segment that starts in it in its second place
-  auto part = [&](int c) { return p.partial + ((long long)c * 2 + (c == c0)) * kStride; };
-  for (int r = warp; r < rows; r += THREADS / 32) {
-    float m = -INFINITY;
-    for (int j = lane; j < parts; j += 32) m = fmaxf(m, __ldcg(part(c0 + j) + RT * DP + r));
+  const int sub = warp % kSplit;
+  const int r = blockIdx.y * kRowsHere + warp / kSplit;
+  const int parts = g.c1 - (int)blockIdx.x + 1;
+  if (blockIdx.y * kRowsHere >= g.rows) return;
+  const bool on = r < g.rows;
+  auto part = [&](int j) { return att_part<DP, RT>(p, blockIdx.x + j, j == 0); };
+  float m = -INFINITY, l = 0.f, acc[kV];
+#pragma unroll
+  for (int e = 0; e < kV; ++e) acc[e] = 0.f;
+  if (on) {
+    for (int j = lane * kSplit + sub; j < parts; j += 32 * kSplit)
+      m = fmaxf(m, part(j)[RT * DP + r]);
     m = warp_max(m);
-    float l = 0.f, acc[VPL];
-#pragma unroll
-    for (int e = 0; e < VPL; ++e) acc[e] = 0.f;
-    for (int j0 = 0; j0 < parts; j0 += 32) {
+    const float ms = m == -INFINITY ? 0.f : m;
+    for (int j0 = sub; j0 < parts; j0 += 32 * kSplit) {
+      const int j = j0 + lane * kSplit;
       float w = 0.f;
-      if (j0 + lane < parts) {
-        float* t = part(c0 + j0 + lane) + RT * DP + r;
-        w = exp2f(__ldcg(t) - m);
-        l += w * __ldcg(t + RT);
-        __stcg(t, 0.f);
-        __stcg(t + RT, 0.f);
+      if (j < parts) {
+        const float* t = part(j) + RT * DP + r;
+        w = exp2f(t[0] - ms);
+        l += w * t[RT];
       }
-      const int cnt = min(32, parts - j0);
-#pragma unroll 8
-      for (int j = 0; j < cnt; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, w, j);
-        float* t = part(c0 + j0 + j) + r * DP + lane * VPL;
-        if constexpr (VPL == 2) {
-          const float2 x = __ldcg(reinterpret_cast<float2*>(t));
-          acc[0] += wj * x.x, acc[1] += wj * x.y;
-          __stcg(reinterpret_cast<float2*>(t), make_float2(0.f, 0.f));
-        } else {
+      const int count = min(32, (parts - j0 + kSplit - 1) / kSplit);
+      for (int i0 = 0; i0 < count; i0 += kBatch) {
+        float x[kBatch][kV];
 #pragma unroll
-          for (int e = 0; e < VPL; e += 4) {
-            const float4 x = __ldcg(reinterpret_cast<float4*>(t + e));
-            acc[e] += wj * x.x, acc[e + 1] += wj * x.y;
-            acc[e + 2] += wj * x.z, acc[e + 3] += wj * x.w;
-            __stcg(reinterpret_cast<float4*>(t + e), make_float4(0.f, 0.f, 0.f, 0.f));
+        for (int i = 0; i < kBatch; ++i) {
+          const float* t = part(j0 + min(i0 + i, count - 1) * kSplit) + r * DP + lane * kV;
+#pragma unroll
+          for (int e = 0; e < kV; e += 2) {
+            if constexpr (kV == 2) {
+              const float2 y = *reinterpret_cast<const float2*>(t);
+              x[i][0] = y.x, x[i][1] = y.y;
+            } else if (e % 4 == 0) {
+              const float4 y = *reinterpret_cast<const float4*>(t + e);
+              x[i][e] = y.x, x[i][e + 1] = y.y, x[i][e + 2] = y.z, x[i][e + 3] = y.w;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
+          if (i0 + i < count) {
+#pragma unroll
+            for (int e = 0; e < kV; ++e) acc[e] += wi * x[i][e];
           }
         }
       }
     }
     l = warp_add(l);
-    const long long o = att_out_row(p, b, h, row0 + r);
-    T* out = static_cast<T*>(p.out) + o * p.d;
-    const float inv = 1.f / l;
+  }
+  if constexpr (kSplit > 1) {
+    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
 #pragma unroll
-    for (int e = 0; e < VPL; ++e)
-      if (lane * VPL + e < p.d) out[lane * VPL + e] = from_f32<T>(acc[e] * inv);
-    if (lane == 0 && p.lse) p.lse[o] = (m + log2f(l)) * kLn2;
-  }
-}
-
-// After a block's part of a shared segment is in the workspace: counts it, and
-// the last block joins.  `flag` is one shared int.
-template <class T, int DP, int RT, int THREADS>
-__device__ __forceinline__ void att_arrive(const AttendParams& p, const AttShare& s, int b, int h,
-                                           int row0, int rows, long long seg_u0, long long seg_u1,
-                                           int* flag) {
-  const int c0 = s.block_of(seg_u0), c1 = s.block_of(seg_u1 - 1);
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const uint32_t before = atomicAdd(p.counters + c0, 1u);
-    *flag = before == (uint32_t)(c1 - c0);
-    if (*flag) {
-      p.counters[c0] = 0;
-      __threadfence();
+    for (int e = 0; e < kV; ++e) s_o[warp][lane * kV + e] = acc[e];
+    __syncthreads();
+    if (sub != 0 || !on) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kSplit; ++i) top = fmaxf(top, s_m[warp + i]);
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < kV; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSplit; ++i) {
+      if (sub + i >= parts) break;  // a warp without parts
+      const float f = top == -INFINITY ? 1.f : exp2f(s_m[warp + i] - top);
+      l += f * s_l[warp + i];
+#pragma unroll
+      for (int e = 0; e < kV; ++e) acc[e] += f * s_o[warp + i][lane * kV + e];
     }
+    m = top;
   }
-  __syncthreads();
-  if (*flag) att_join<T, DP, RT, THREADS>(p, b, h, row0, rows, c0, c1);
+  if (!on) return;
+  const long long row = att_out_row(p, g.b, g.h, g.row0 + r);
+  T* out = static_cast<T*>(p.out) + row * p.d;
+  const float inv = 1.f / l;
+#pragma unroll
+  for (int e = 0; e < kV; ++e)
+    if (lane * kV + e < p.d) out[lane * kV + e] = from_f32<T>(acc[e] * inv);
+  if (lane == 0 && p.lse) p.lse[row] = (m + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------------------
@@ -336,7 +392,7 @@ struct GenSmem {
   float alpha[kGenR], m[kGenR], l[kGenR];
   const unsigned char* row_k[kGenU];
   const unsigned char* row_v[kGenU];
-  int bad, flag;
+  int bad;
   alignas(16) unsigned char share[kShareBytes];
 };
 
@@ -347,9 +403,10 @@ __global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const Atten
   constexpr int kRG = DP == 64 ? 2 : 1;            // thread groups over the rows
   constexpr int kRows = kGenR / kRG;               // rows of a thread
   constexpr int kCols = DP == 256 ? 2 : 1;         // columns of a thread
-  constexpr int kStride = att_partial_floats(kGenR, DP);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int col = tid % (kGenThreads / kRG), rg = tid / (kGenThreads / kRG) * kRows;
+  if (tid == 0) att_clear_note(p);
+  pdl_launch_dependents();
   AttCursor<kGenU, kGenR> cur;
   const AttShare s = att_share<kGenU, kGenR, kGenThreads>(p, cur, sm.share);
   const T* kc = static_cast<const T*>(p.k);
@@ -543,8 +600,7 @@ __global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const Atten
         if (col == 0 && p.lse) p.lse[o] = (sm.m[rg + r] + log2f(ll)) * kLn2;
       }
     } else {
-      const long long seg_u0 = u - tile0, seg_u1 = seg_u0 + cur.tiles;
-      float* t = p.partial + ((long long)blockIdx.x * 2 + (tile0 == 0 ? 1 : 0)) * kStride;
+      float* t = att_part<DP, kGenR>(p, blockIdx.x, tile0 == 0);
 #pragma unroll
       for (int r = 0; r < kRows; ++r)
 #pragma unroll
@@ -554,7 +610,8 @@ __global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const Atten
         __stcg(t + kGenR * DP + tid, sm.m[tid]);
         __stcg(t + kGenR * DP + kGenR + tid, bad ? nan : sm.l[tid]);
       }
-      att_arrive<T, DP, kGenR, kGenThreads>(p, s, cur.b, h, row0, rows, seg_u0, seg_u1, &sm.flag);
+      if (tid == 0 && tile0 == 0)
+        att_note(p, s, cur.b, h, row0, rows, u + cur.tiles);
     }
     u += cnt;
     if (tile0 + cnt == cur.tiles)
@@ -562,7 +619,7 @@ __global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const Atten
     else
       cur.tile += cnt;
   }
-  att_fill_padding<T, kGenThreads>(p);
+  att_fill_padding<T>(p, 0, kGenThreads / 32);
 }
 
 }  // namespace sv

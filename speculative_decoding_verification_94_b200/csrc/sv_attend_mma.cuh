@@ -34,7 +34,7 @@ struct MmaCfg {
   static constexpr int kCols = 64 / MT;                    // output columns added at a time
   static constexpr int kRing = kMmaWarps * kStages * kStage;
   static constexpr int kMerge = kMmaWarps * kRows * kCols * 4;
-  static constexpr int kSmem = kRing + kMerge + 16;  // two blocks an SM
+  static constexpr int kSmem = kRing + kMerge;  // two blocks an SM
 };
 
 // 16 bytes, or zeros.
@@ -107,16 +107,16 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
   constexpr int kRows = C::kRows, kStages = C::kStages;
   constexpr int kChunks = D / 8;              // 16-byte chunks of a row
   constexpr int kPerCopy = 32 / kChunks;      // rows that a warp's 32 lanes copy at once
-  constexpr int kPart = att_partial_floats(kRows, D);
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   unsigned char* ring = smem + warp * kStages * C::kStage;
   float* merge = reinterpret_cast<float*>(smem + C::kRing);
   float2* s_ml = reinterpret_cast<float2*>(merge);  // [warp][row] (m, l), before the outputs
-  int* s_flag = reinterpret_cast<int*>(smem + C::kRing + C::kMerge);
   const __nv_bfloat16* kc = static_cast<const __nv_bfloat16*>(p.k);
   const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(p.v);
 
+  if (tid == 0) att_clear_note(p);
+  pdl_launch_dependents();
   AttCursor<kMmaU, kRows> cur;
   const AttShare s = att_share<kMmaU, kRows, kMmaThreads>(p, cur, merge);
 
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
       sum += top == -INFINITY ? ml.y : pow2(ml.x - top) * ml.y;
     }
     const bool whole = tile0 == 0 && cnt == cur.tiles;
-    float* part = p.partial + ((long long)blockIdx.x * 2 + (tile0 == 0 ? 1 : 0)) * kPart;
+    float* part = att_part<D, kRows>(p, blockIdx.x, tile0 == 0);
     const long long orow_at = att_out_row(p, cur.b, h, row0 + min(orow, rows - 1));
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += C::kCols) {
@@ -446,11 +446,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
         __stcg(part + kRows * D + kRows + orow, sum);
       }
     }
-    if (!whole) {
-      const long long seg_u0 = u - tile0, seg_u1 = seg_u0 + cur.tiles;
-      att_arrive<__nv_bfloat16, D, kRows, kMmaThreads>(p, s, cur.b, h, row0, rows, seg_u0, seg_u1,
-                                                       s_flag);
-    }
+    if (!whole && tile0 == 0 && tid == 0)
+      att_note(p, s, cur.b, h, row0, rows, u + cur.tiles);
     __syncthreads();  // merge is free again
     u += cnt;
     if (tile0 + cnt == cur.tiles)
@@ -459,7 +456,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
       cur.tile += cnt;
   }
   cp_async_wait<0>();
-  att_fill_padding<__nv_bfloat16, kMmaThreads>(p);
+  att_fill_padding<__nv_bfloat16>(p, 0, kMmaWarps);
 }
 
 }  // namespace sv

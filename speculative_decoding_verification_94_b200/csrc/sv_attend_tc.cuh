@@ -11,7 +11,8 @@
 // end.  The products take the same time whatever RT is, 0.5 us of the 1.5 us
 // in which one SM's share of HBM brings the 64 KB of a tile.
 //
-// Roles.  One warp issues the copies, one the products.  Two warp groups take
+// Roles.  One warp issues the copies, one the products, two fill the rows
+// behind a request's own.  Two warp groups take
 // the even and the odd tiles, each with its own S, P, O, maximum and sum, so
 // that one's softmax runs under the other's products, and neither waits for
 // the other.  O stays in tensor memory; it is rescaled only when the maximum
@@ -34,7 +35,7 @@ namespace sv {
 
 constexpr int kTcU = 128;            // keys of a tile
 constexpr int kTcSoftmax = 256;      // threads of the two warp groups
-constexpr int kTcThreads = 320;      // + copy warp + product warp
+constexpr int kTcThreads = 384;      // + copy warp, product warp, two for the rest
 constexpr int kTcStages = 3;
 
 template <int D>
@@ -161,7 +162,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   using C = TcCfg<D>;
   constexpr int kCopies = 128 / RT;          // copies of a row among the lanes
   constexpr int kKeys = kTcU / kCopies;      // keys of a copy
-  constexpr int kPart = att_partial_floats(RT, D);
   extern __shared__ __align__(1024) unsigned char smem[];
   const AttendParams& p = tp.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -174,7 +174,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   volatile int* s_abort = misc;      // a wait ran out
   int* s_bad = misc + 1;             // the segment's keys are on a bad page
   int* s_fix = misc + 2;             // a new token's value is not finite
-  int* s_flag = misc + 3;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc + 4);
 
   if (tid == 0) {
@@ -192,6 +191,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(q_full, kTcSoftmax);
     fence_mbar_init();
     misc[0] = misc[1] = misc[2] = 0;
+    att_clear_note(p);
   }
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tc_fence_before();
   }
+  pdl_launch_dependents();
   AttCursor<kTcU, RT> cur;
   const AttShare s = att_share<kTcU, RT, kTcThreads>(p, cur, smem + C::kOffShare);
   __syncthreads();
@@ -319,6 +320,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
     __syncwarp();
+  } else if (warp >= 10) {
+    att_fill_padding<__nv_bfloat16>(p, 10, 2);
   } else {
     // ------------------------------- softmax -------------------------------
     const int w = warp >> 2, quad = warp & 3;
@@ -356,13 +359,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           *reinterpret_cast<uint4*>(s_q + (c / 8) * C::kHalf + r * 128 +
                                     (((c % 8) ^ (r & 7)) << 4)) = x[j];
         }
-        const int first = (int)((long long)tile0 * kTcU / p.page);
-        const int last = (int)((min((long long)(tile0 + cnt) * kTcU, (long long)len) - 1) / p.page);
-        for (int j = first + tid; j <= last; j += kTcSoftmax) {
-          const int id = __ldg(trow + j);
-          if (id < 0 || id >= p.num_pages) *s_bad = 1;
-        }
       }
+      // the pages of these tiles: loaded here, looked at when the tiles are done
+      const int page0 = tile0 * kTcU / p.page;
+      const int pages = (min((tile0 + cnt) * kTcU, len) - 1) / p.page + 1 - page0;
+      const int id0 = tid < pages ? __ldg(trow + page0 + tid) : 0;
+      const int id1 = tid + kTcSoftmax < pages ? __ldg(trow + page0 + tid + kTcSoftmax) : 0;
       fence_async_smem();
       tc_fence_before();
       mbar_arrive(q_full);
@@ -522,6 +524,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (row < rows) kv_flag(p.status, SV_DEV_BAD_TREE);
       }
       s_ml[w * 128 + lr] = make_float2(m, l);
+      bool off = (unsigned)id0 >= (unsigned)p.num_pages || (unsigned)id1 >= (unsigned)p.num_pages;
+      for (int j = tid + 2 * kTcSoftmax; j < pages; j += kTcSoftmax)
+        off |= (unsigned)__ldg(trow + page0 + j) >= (unsigned)p.num_pages;
+      if (off) *s_bad = 1;
       softmax_sync();
       const bool gone = __any_sync(0xffffffffu, *s_abort != 0);
       const bool bad = *s_bad != 0, fix = *s_fix != 0;
@@ -544,9 +550,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       row_stats(row, top, sum);
       const float f = top == -INFINITY ? 0.f : pow2(m - top);
       const bool whole = tile0 == 0 && cnt == cur.tiles;
-      float* part = p.partial + ((long long)blockIdx.x * 2 + (tile0 == 0 ? 1 : 0)) * kPart;
+      float* part = att_part<D, RT>(p, blockIdx.x, tile0 == 0);
       float* stage = reinterpret_cast<float*>(s_q);  // [2][128][kCols]
       constexpr int kPieces = C::kCols / 4;
+      // a thread adds the same piece of the same rows in every round
+      constexpr int kRowStep = kTcSoftmax / kPieces, kMine = (RT + kRowStep - 1) / kRowStep;
+      const int piece = tid % kPieces, r_first = tid / kPieces;
+      float inv[kMine];
+      long long out_at[kMine];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int r = r_first + i * kRowStep;
+        inv[i] = 0.f;
+        out_at[i] = 0;
+        if (r < rows) {
+          float rt, rs;
+          row_stats(r, rt, rs);
+          inv[i] = 1.f / rs;
+          out_at[i] = whole ? att_out_row(p, cur.b, h, row0 + r) * D : (long long)r * D;
+        }
+      }
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += C::kCols) {
         float4* dst = reinterpret_cast<float4*>(stage + (w * 128 + lr) * C::kCols);
@@ -578,8 +601,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int j = 0; j < kPieces; ++j) dst[j] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         softmax_sync();
-        for (int it = tid; it < rows * kPieces; it += kTcSoftmax) {
-          const int r = it / kPieces, j = it % kPieces;
+#pragma unroll
+        for (int n = 0; n < kMine; ++n) {
+          const int r = r_first + n * kRowStep, j = piece;
+          if (r >= rows) continue;
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int q = 0; q < 2 * kCopies; ++q) {
@@ -613,16 +638,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
           if (whole) {
-            float rt, rs;
-            row_stats(r, rt, rs);
-            const float inv = 1.f / rs;
             uint2 y;
-            y.x = pack_bf16(a.x * inv, a.y * inv);
-            y.y = pack_bf16(a.z * inv, a.w * inv);
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) +
-                                      att_out_row(p, cur.b, h, row0 + r) * D + col) = y;
+            y.x = pack_bf16(a.x * inv[n], a.y * inv[n]);
+            y.y = pack_bf16(a.z * inv[n], a.w * inv[n]);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + out_at[n] + col) = y;
           } else {
-            __stcg(reinterpret_cast<float4*>(part + r * D + col), a);
+            __stcg(reinterpret_cast<float4*>(part + out_at[n] + col), a);
           }
         }
         softmax_sync();
@@ -635,23 +656,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           __stcg(part + RT * D + RT + lr, sum);
         }
       }
-      if (!whole) {
-        const long long seg_u0 = u - tile0, seg_u1 = seg_u0 + cur.tiles;
-        const int c0 = s.block_of(seg_u0), c1 = s.block_of(seg_u1 - 1);
-        __threadfence();
-        softmax_sync();
-        if (tid == 0) {
-          const uint32_t before = atomicAdd(p.counters + c0, 1u);
-          *s_flag = before == (uint32_t)(c1 - c0);
-          if (*s_flag) {
-            p.counters[c0] = 0;
-            __threadfence();
-          }
-        }
-        softmax_sync();
-        if (*s_flag)
-          att_join<__nv_bfloat16, D, RT, kTcSoftmax>(p, cur.b, h, row0, rows, c0, c1);
-      }
+      if (!whole && tile0 == 0 && tid == 0)
+        att_note(p, s, cur.b, h, row0, rows, u + cur.tiles);
       tc_fence_before();
       if (tid == 0) *s_bad = *s_fix = 0;
       softmax_sync();  // before the next segment's q and flags
@@ -668,7 +674,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
-  att_fill_padding<__nv_bfloat16, kTcThreads>(p);
 }
 
 }  // namespace sv

@@ -64,11 +64,11 @@ cudaError_t launch(K kernel, const Prm& prm, dim3 grid, int threads, int smem, c
 }
 
 // ---------------------------------------------------------------------------
-// Attention: grid and workspace
+// Attention: grid and scratch
 // ---------------------------------------------------------------------------
 int padded_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-constexpr size_t kCounterBytes = (4 * kAttMaxBlocks + 255) / 256 * 256;
+constexpr size_t kSharedBytes = (sizeof(AttShared) * kAttMaxBlocks + 255) / 256 * 256;
 
 // Rows of a row tile, which set the size of a partial result.  16 also covers
 // the general kernel, which any bf16 call may need for its strides.
@@ -77,13 +77,32 @@ int tile_rows(int rows, int head_dim, sv_dtype dt) {
   return rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
 
-size_t attend_ws(int rows, int head_dim, sv_dtype dt) {
-  return kCounterBytes + (size_t)kAttMaxBlocks * 2 *
+size_t attend_scratch(int rows, int head_dim, sv_dtype dt) {
+  return kSharedBytes + (size_t)kAttMaxBlocks * 2 *
                              att_partial_floats(tile_rows(rows, head_dim, dt), padded_dim(head_dim)) *
                              4;
 }
 
-template <class K>
+// The second launch: its blocks are on the device before the first ends.
+template <class T, int DP, int RT>
+cudaError_t launch_join(const AttendParams& p, int grid, cudaStream_t s) {
+  constexpr int kRowsHere = RT >= 128 ? 4 : RT == 64 ? 2 : 1;
+  const int rows = std::min(RT, p.n * p.g);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)((rows + kRowsHere - 1) / kRowsHere));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = launch_mark_before(s);
+  if (e != cudaSuccess) return e;
+  return launch_mark_after(s, cudaLaunchKernelEx(&cfg, attend_join_kernel<T, DP, RT>, p));
+}
+
+template <class T, int DP, int RT, class K>
 cudaError_t launch_attend(K kernel, AttendParams& p, int threads, int smem, cudaStream_t s) {
   const void* kp = reinterpret_cast<const void*>(kernel);
   cudaError_t e = ensure_kernel_attrs(kp, smem, false);
@@ -93,20 +112,22 @@ cudaError_t launch_attend(K kernel, AttendParams& p, int threads, int smem, cuda
   if ((e = sm_count(&sms)) != cudaSuccess) return e;
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
   const int grid = std::min(per_sm * sms, kAttMaxBlocks);
-  return launch(kernel, p, dim3((unsigned)grid), threads, smem, s);
+  if ((e = launch(kernel, p, dim3((unsigned)grid), threads, smem, s)) != cudaSuccess) return e;
+  return launch_join<T, DP, RT>(p, grid, s);
 }
 
 template <class T, bool VEC>
 cudaError_t launch_general(AttendParams& p, cudaStream_t s) {
   switch (padded_dim(p.d)) {
     case 64:
-      return launch_attend(attend_general_kernel<T, 64, VEC>, p, kGenThreads, sizeof(GenSmem<64>), s);
+      return launch_attend<T, 64, kGenR>(attend_general_kernel<T, 64, VEC>, p, kGenThreads,
+                                           sizeof(GenSmem<64>), s);
     case 128:
-      return launch_attend(attend_general_kernel<T, 128, VEC>, p, kGenThreads, sizeof(GenSmem<128>),
-                           s);
+      return launch_attend<T, 128, kGenR>(attend_general_kernel<T, 128, VEC>, p, kGenThreads,
+                                           sizeof(GenSmem<128>), s);
     default:
-      return launch_attend(attend_general_kernel<T, 256, VEC>, p, kGenThreads, sizeof(GenSmem<256>),
-                           s);
+      return launch_attend<T, 256, kGenR>(attend_general_kernel<T, 256, VEC>, p, kGenThreads,
+                                           sizeof(GenSmem<256>), s);
   }
 }
 
@@ -161,8 +182,10 @@ cudaError_t launch_tc(const TcParams& tp, const CUtensorMap& km, const CUtensorM
   int sms = 0;
   if ((e = sm_count(&sms)) != cudaSuccess) return e;
   if ((e = launch_mark_before(s)) != cudaSuccess) return e;
-  kernel<<<(unsigned)std::min(sms, kAttMaxBlocks), kTcThreads, TcCfg<D>::kSmem, s>>>(tp, km, vm);
-  return launch_mark_after(s, cudaGetLastError());
+  const int grid = std::min(sms, kAttMaxBlocks);
+  kernel<<<(unsigned)grid, kTcThreads, TcCfg<D>::kSmem, s>>>(tp, km, vm);
+  if ((e = launch_mark_after(s, cudaGetLastError())) != cudaSuccess) return e;
+  return launch_join<__nv_bfloat16, D, RT>(tp.a, grid, s);
 }
 
 template <int D>
@@ -178,8 +201,10 @@ template <int D>
 cudaError_t launch_mma(AttendParams& p, cudaStream_t s) {
   // a second row tile of 16 only where there are rows for it
   if (p.n * p.g <= 16)
-    return launch_attend(attend_mma_kernel<D, 1>, p, kMmaThreads, MmaCfg<D, 1>::kSmem, s);
-  return launch_attend(attend_mma_kernel<D, 2>, p, kMmaThreads, MmaCfg<D, 2>::kSmem, s);
+    return launch_attend<__nv_bfloat16, D, 16>(attend_mma_kernel<D, 1>, p, kMmaThreads,
+                                               MmaCfg<D, 1>::kSmem, s);
+  return launch_attend<__nv_bfloat16, D, 32>(attend_mma_kernel<D, 2>, p, kMmaThreads,
+                                             MmaCfg<D, 2>::kSmem, s);
 }
 
 }  // namespace
@@ -281,20 +306,20 @@ sv_status sv_kv_append(const sv_kv_cache* cache, const void* k, const void* v, i
   }
 }
 
-size_t sv_kv_attend_workspace_size(int B, int n, int q_heads, int heads, int head_dim,
+size_t sv_kv_attend_scratch_size(int B, int n, int q_heads, int heads, int head_dim,
                                    sv_dtype dtype) {
   if (B < 0 || n < 1 || heads < 1 || q_heads < 1 || head_dim < 1 || head_dim > 256 ||
       (dtype != SV_F32 && dtype != SV_BF16))
     return 0;
   if (n > 1024 || q_heads % heads) return 0;
-  return attend_ws(n * (q_heads / heads), head_dim, dtype);
+  return attend_scratch(n * (q_heads / heads), head_dim, dtype);
 }
 
 sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_stride,
                        int64_t token_stride, int B, int n, int q_heads, const int32_t* block_table,
                        int max_pages, const int32_t* kv_len, const int32_t* q_len,
-                       const int32_t* parents, float scale, void* out, float* lse, void* workspace,
-                       size_t workspace_bytes, int32_t* device_status, void* stream) {
+                       const int32_t* parents, float scale, void* out, float* lse, void* scratch,
+                       size_t scratch_bytes, int32_t* device_status, void* stream) {
   if (B < 0 || n < 1 || n > 1024 || q_heads < 1 || max_pages < 1) return SV_ERR_INVALID_ARG;
   const sv_status st = check_cache(cache);
   if (st != SV_OK) return st;
@@ -311,9 +336,9 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_st
       !aligned_or_null(device_status, 4))
     return SV_ERR_INVALID_ARG;
   if (q_heads > (1 << 16) || (long long)B * n > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
-  if (!workspace || !aligned(workspace, 16) ||
-      workspace_bytes <
-          attend_ws(n * (q_heads / cache->heads), cache->head_dim, cache->dtype))
+  if (!scratch || !aligned(scratch, 16) ||
+      scratch_bytes <
+          attend_scratch(n * (q_heads / cache->heads), cache->head_dim, cache->dtype))
     return SV_ERR_WORKSPACE;
   AttendParams p = {};
   p.q = q;
@@ -339,8 +364,8 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_st
   p.c_token = cache->token_stride;
   p.c_head = cache->head_stride;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  p.counters = static_cast<uint32_t*>(workspace);
-  p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kCounterBytes);
+  p.shared = static_cast<AttShared*>(scratch);
+  p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + kSharedBytes);
   p.status = device_status;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool vec = common_width({addr(cache->k), addr(cache->v), p.c_page * es, p.c_token * es,

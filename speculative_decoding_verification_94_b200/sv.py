@@ -41,7 +41,7 @@ EXPORTS = ("sv_verify_chain", "sv_verify_chain_ragged", "sv_verify_chain_noalloc
            "sv_verify_tree_sample", "sv_extract_topk_kd", "sv_kd_kl_loss", "sv_sched_select",
            "sv_verify_chain_workspace_size", "sv_verify_tree_workspace_size",
            "sv_extract_topk_workspace_size", "sv_kd_kl_loss_workspace_size",
-           "sv_kv_plan", "sv_kv_append", "sv_kv_attend", "sv_kv_attend_workspace_size",
+           "sv_kv_plan", "sv_kv_append", "sv_kv_attend", "sv_kv_attend_scratch_size",
            "sv_kv_commit",
            "sv_device_status_check", "sv_status_string", "sv_version")
 
@@ -128,8 +128,8 @@ def lib() -> ctypes.CDLL:
             L.sv_kv_attend.argtypes = [vp, vp, i64, i64, ci, ci, ci, vp, ci, vp, vp, vp, cf, vp,
                                        vp, vp, sz, vp, vp]
             L.sv_kv_commit.argtypes = [vp, ci, i64, ci, vp, ci, vp, vp, ci, vp, vp, vp]
-            L.sv_kv_attend_workspace_size.argtypes = [ci, ci, ci, ci, ci, ci]
-            L.sv_kv_attend_workspace_size.restype = sz
+            L.sv_kv_attend_scratch_size.argtypes = [ci, ci, ci, ci, ci, ci]
+            L.sv_kv_attend_scratch_size.restype = sz
             for f in ("sv_kv_plan", "sv_kv_append", "sv_kv_attend", "sv_kv_commit"):
                 getattr(L, f).restype = ci
             L.sv_set_knob.argtypes = [ci, ctypes.c_longlong]
@@ -551,27 +551,10 @@ def sv_kd_grad(topk_logp: torch.Tensor, topk_idx: torch.Tensor, draft: torch.Ten
 # ---------------------------------------------------------------------------
 # The paged key-value cache of a verification step
 # ---------------------------------------------------------------------------
-_KV_WS: dict = {}  # (device, stream) -> workspace of the calls on that stream
-
-
 def _on(dev: torch.device, stream):
     """Context of a call: `dev` is the current device, which the C calls use,
     and `stream`, if given, the stream of what the binding allocates."""
     return torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream)
-
-
-def _kv_workspace(dev: torch.device, stream: int, nbytes: int) -> torch.Tensor:
-    """Zero-filled workspace for one call.  Calls on one stream run in order,
-    so they share a buffer; a captured call gets its own, from the graph's
-    memory and zeroed by the graph, since graphs may be replayed anywhere."""
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-    key = (dev.index, stream)
-    cur = _KV_WS.get(key)
-    if cur is None or cur.numel() < nbytes:
-        cur = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-        _KV_WS[key] = cur
-    return cur
 
 
 def _ptr(t, name: str, dtype, dev, numel: int | None = None):
@@ -675,22 +658,23 @@ def sv_kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cac
         _check(lib().sv_kv_append(*args, _stream(dev, stream)), "sv_kv_append")
 
 
-def sv_kv_attend_workspace_size(B: int, n: int, q_heads: int, heads: int, head_dim: int,
+def sv_kv_attend_scratch_size(B: int, n: int, q_heads: int, heads: int, head_dim: int,
                                 dtype: torch.dtype) -> int:
     code = SV_BF16 if dtype == torch.bfloat16 else SV_F32
-    return int(lib().sv_kv_attend_workspace_size(B, n, q_heads, heads, head_dim, code))
+    return int(lib().sv_kv_attend_scratch_size(B, n, q_heads, heads, head_dim, code))
 
 
 def sv_kv_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                  block_table: torch.Tensor, kv_len: torch.Tensor, *,
                  q_len: torch.Tensor | None = None, parents: torch.Tensor | None = None,
                  scale: float | None = None, out: dict | None = None,
-                 ws: torch.Tensor | None = None, device_status: torch.Tensor | None = None,
-                 stream=None) -> dict:
+                 scratch: torch.Tensor | None = None,
+                 device_status: torch.Tensor | None = None, stream=None) -> dict:
     """Attention of the new tokens q [B, n, q_heads, head_dim] (a chain, or a
     tree given by parents [B, n]) over the paged cache (see sv.h).  Returns
     out [B, n, q_heads, head_dim] and lse [B, n, q_heads].  scale defaults to
-    head_dim ** -0.5."""
+    head_dim ** -0.5.  scratch: sv_kv_attend_scratch_size bytes for this call
+    (torch's allocator gives them if it is None)."""
     c = _kv_cache(k_cache, v_cache)
     dev, i32 = k_cache.device, torch.int32
     st = _token_rows(q, "q", k_cache, None)
@@ -704,10 +688,9 @@ def sv_kv_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
             o["out"] = torch.empty(B, n, hq, d, dtype=q.dtype, device=dev)
         if "lse" not in o:
             o["lse"] = torch.empty(B, n, hq, dtype=torch.float32, device=dev)
-        s = _stream(dev, stream)
-        if ws is None:
-            nbytes = lib().sv_kv_attend_workspace_size(B, n, hq, k_cache.shape[2], d, c.dtype)
-            ws = _kv_workspace(dev, s.value, nbytes)
+        if scratch is None:
+            nbytes = lib().sv_kv_attend_scratch_size(B, n, hq, k_cache.shape[2], d, c.dtype)
+            scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         _check(lib().sv_kv_attend(
             ctypes.byref(c), q.data_ptr(), st[0], st[1], B, n, hq,
             _ptr(block_table, "block_table", i32, dev), block_table.shape[1],
@@ -715,8 +698,9 @@ def sv_kv_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
             _ptr(parents, "parents", i32, dev, B * n),
             float(d ** -0.5 if scale is None else scale),
             _ptr(o["out"], "out", q.dtype, dev, q.numel()),
-            _ptr(o["lse"], "lse", torch.float32, dev, B * n * hq), ws.data_ptr(), ws.numel(),
-            _ptr(device_status, "device_status", i32, dev), s), "sv_kv_attend")
+            _ptr(o["lse"], "lse", torch.float32, dev, B * n * hq),
+            _ptr(scratch, "scratch", torch.uint8, dev), scratch.numel(),
+            _ptr(device_status, "device_status", i32, dev), _stream(dev, stream)), "sv_kv_attend")
     return o
 
 

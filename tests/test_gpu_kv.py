@@ -405,15 +405,17 @@ def test_attend_offsets_past_32_bits():
     assert torch.equal(k[2, 5], x[0, 0]) and torch.equal(v[2, 5], x[0, 0])
 
 
-def test_attend_repeats_bit_for_bit_and_returns_its_workspace_to_zero():
-    for n, hq, lens in ((1, 4, [9000, 30, 1]), (4, 16, [5000, 77, 3]), (20, 16, [2000, 9, 4000])):
-        s = scenario(3, n, hq, 2, 128, 16, lens, "bf16", seed=2)
-        nb = sv.sv_kv_attend_workspace_size(3, n, hq, 2, 128, torch.bfloat16)
-        ws = torch.zeros(nb, dtype=torch.uint8, device=DEV)
-        first = call_attend(s, ws=ws)
-        assert int(ws.count_nonzero().item()) == 0
-        for _ in range(3):
-            again = call_attend(s, ws=ws)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attend_repeats_bit_for_bit_whatever_its_scratch_holds(dtype):
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    for n, hq, lens in ((1, 4, [9000, 30, 1]), (4, 16, [5000, 77, 3]), (8, 16, [5000, 77, 3]),
+                        (20, 16, [2000, 9, 4000])):
+        s = scenario(3, n, hq, 2, 128, 16, lens, dtype, seed=2)
+        nb = sv.sv_kv_attend_scratch_size(3, n, hq, 2, 128, dt)
+        first = call_attend(s)
+        for fill in (0, 0x7F, 0xFF):
+            scratch = torch.full((nb,), fill, dtype=torch.uint8, device=DEV)
+            again = call_attend(s, scratch=scratch)
             assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
 
 
@@ -546,7 +548,7 @@ def test_binding_refuses_mismatched_tensors():
     with pytest.raises(TypeError):
         attend(l=l.long())
     with pytest.raises(sv.SVError) as e:
-        attend(ws=torch.zeros(16, dtype=torch.uint8, device=DEV))
+        attend(scratch=torch.zeros(16, dtype=torch.uint8, device=DEV))
     assert e.value.status == sv.SV_ERR_WORKSPACE
     with pytest.raises(sv.SVError) as e:
         attend(q=s["q"][:, :, :3].contiguous())  # 3 query heads over 2 key heads

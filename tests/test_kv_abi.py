@@ -99,12 +99,12 @@ def test_attend_validates(lib):
                dict(bs=-1), dict(ts=-1)):
         assert call(**kw) == E, kw
     assert call(hq=1 << 17) == U
-    need = lib.sv_kv_attend_workspace_size(4, 4, 4, 2, 64, sv.SV_BF16)
+    need = lib.sv_kv_attend_scratch_size(4, 4, 4, 2, 64, sv.SV_BF16)
     assert need > 0
     assert call(ws=None) == W and call(ws=F + 8) == W and call(wsb=need - 1) == W
     assert call(B=0, ws=None) == sv.SV_OK
-    assert lib.sv_kv_attend_workspace_size(4, 4, 4, 2, 257, sv.SV_BF16) == 0
-    assert lib.sv_kv_attend_workspace_size(4, 0, 4, 2, 64, sv.SV_BF16) == 0
+    assert lib.sv_kv_attend_scratch_size(4, 4, 4, 2, 257, sv.SV_BF16) == 0
+    assert lib.sv_kv_attend_scratch_size(4, 0, 4, 2, 64, sv.SV_BF16) == 0
 
 
 @no_gpu
