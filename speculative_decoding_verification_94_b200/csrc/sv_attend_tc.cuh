@@ -11,8 +11,8 @@
 // end.  The products take the same time whatever RT is, 0.5 us of the 1.5 us
 // in which one SM's share of HBM brings the 64 KB of a tile.
 //
-// Roles.  One warp issues the copies, one the products, two fill the rows
-// behind a request's own.  Two warp groups take
+// Roles.  Two warps issue the copies (keys, values), one the products, one
+// fills the rows behind a request's own.  Two warp groups take
 // the even and the odd tiles, each with its own S, P, O, maximum and sum, so
 // that one's softmax runs under the other's products, and neither waits for
 // the other.  O stays in tensor memory; it is rescaled only when the maximum
@@ -35,7 +35,7 @@ namespace sv {
 
 constexpr int kTcU = 128;            // keys of a tile
 constexpr int kTcSoftmax = 256;      // threads of the two warp groups
-constexpr int kTcThreads = 384;      // + copy warp, product warp, two for the rest
+constexpr int kTcThreads = 384;      // + two copy warps, product warp, one for the rest
 constexpr int kTcStages = 3;
 
 template <int D>
@@ -73,6 +73,17 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok;
 }
 // D = A B (+ D): A and B in shared memory.
 __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -207,12 +218,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  if (warp == 8) {
-    // ------------------------------ copies --------------------------------
+  if (warp == 8 || warp == 10) {
+    // ---------------- copies: keys (warp 8) and values (warp 10) ---------------
+    // apart, because keys are done with two tiles before values are
+    const bool keys = warp == 8;
     const int boxes = kTcU / tp.box;              // <= 16 per 64 columns
     constexpr int kHalves = D / 64;
     const int bi = lane & 15, half = lane >> 4;
     const bool mine = bi < boxes && half < kHalves;
+    uint64_t *fulls = keys ? k_full : v_full, *empties = keys ? k_empty : v_empty;
+    unsigned char* ring = smem + (keys ? C::kOffK : C::kOffV) + half * C::kHalf + bi * tp.box * 128;
     long long u = s.u0;
     auto page_of = [&]() {  // out of the pool: zeros are copied
       const int pos = cur.tile * kTcU + bi * tp.box;
@@ -223,37 +238,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int page = page_of();
     int slot = 0, round = 0;
     bool ok = true;
-    for (; u < s.u1 && ok;) {
+    while (u < s.u1) {
       const int h = cur.seg / cur.mt;
       const int token = (cur.tile * kTcU + bi * tp.box) % p.page;
-      const uint32_t off = half * C::kHalf + bi * tp.box * 128;
       const int id = page;
       ++u;
       cur.advance(p);
       page = page_of();
-      for (int kvs = 0; kvs < 2; ++kvs) {
-        uint64_t* full = (kvs ? v_full : k_full) + slot;
-        uint64_t* empty = (kvs ? v_empty : k_empty) + slot;
-        if (round) ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty, (round - 1) & 1));
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(full, C::kTile);
-        __syncwarp();
-        if (mine) {
-          if (kvs == 0)
-            tma_page(smem + C::kOffK + slot * C::kTile + off, &kmap, half * 64, token, h, id, full);
-          else
-            tma_page(smem + C::kOffV + slot * C::kTile + off, &vmap, half * 64, token, h, id, full);
-        }
+      if (round) ok = __all_sync(0xffffffffu, mbar_wait_bounded(empties + slot, (round - 1) & 1));
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(fulls + slot, C::kTile);
+      __syncwarp();
+      if (mine) {
+        unsigned char* dst = ring + slot * C::kTile;
+        if (keys)
+          tma_page(dst, &kmap, half * 64, token, h, id, fulls + slot);
+        else
+          tma_page(dst, &vmap, half * 64, token, h, id, fulls + slot);
       }
       if (++slot == kTcStages) slot = 0, ++round;
     }
     if (!ok) {  // the copies under way end before the block does
       *s_abort = 1;
       kv_flag(p.status, SV_DEV_TIMEOUT);
-      for (int i = 0; i < kTcStages; ++i) {
-        mbar_wait_bounded(k_full + i, (round - (i >= slot)) & 1);
-        mbar_wait_bounded(v_full + i, (round - (i >= slot)) & 1);
-      }
+      for (int i = 0; i < kTcStages; ++i)
+        mbar_wait_bounded(fulls + i, (round - (i >= slot)) & 1);
     }
   } else if (warp == 9) {
     // ------------------------------ products ------------------------------
@@ -264,49 +273,63 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int streams[2] = {0, 0};  // tiles of each warp group
       int segs = 0;
       bool ok = true;
-      auto qk = [&](int w) {
-        const int slot = kg % kTcStages;
-        ok = ok && mbar_wait_bounded(k_full + slot, (kg / kTcStages) & 1);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t ka = smem_u32(smem + C::kOffK + slot * C::kTile);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t o = (ks / 4) * C::kHalf + (ks % 4) * 32;
-          tc_mma_ss(tmem + w * 128, tc_desc(qa + o, 16), tc_desc(ka + o, 16), kIdQk, ks > 0);
-        }
-        tc_commit(s_full + w);
-        tc_commit(k_empty + slot);
-        ++kg;
-      };
       for (long long u = s.u0; u < s.u1 && ok;) {
         const int left = cur.tiles - cur.tile;
         const int cnt = s.u1 - u < left ? (int)(s.u1 - u) : left;
         ok = mbar_wait_bounded(q_full, segs & 1);
         ++segs;
         if (!ok) break;
-        qk(0);
-        if (cnt > 1) qk(1);
-        for (int k = 0; k < cnt && ok; ++k) {
-          const int w = k & 1;
-          ok = mbar_wait_bounded(p_ready + w, streams[w] & 1);
-          ++streams[w];
-          const int slot = vg % kTcStages;
-          ok = ok && mbar_wait_bounded(v_full + slot, (vg / kTcStages) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t va = smem_u32(smem + C::kOffV + slot * C::kTile);
-          const uint32_t pa = tmem + w * 128, o = tmem + 256 + w * 128;
+        tc_fence_after();
+        // whichever product has its operands: S of tile nq (its warp group's
+        // last P is used up), or P V of tile np
+        int nq = 0, np = 0;
+        uint64_t t0 = globaltimer_ns();
+        while (np < cnt) {
+          bool idle = true;
+          if (np < nq) {
+            const int w = np & 1, slot = vg % kTcStages;
+            if (mbar_test(p_ready + w, streams[w] & 1) &&
+                mbar_test(v_full + slot, (vg / kTcStages) & 1)) {
+              tc_fence_after();
+              const uint32_t va = smem_u32(smem + C::kOffV + slot * C::kTile);
+              const uint32_t pa = tmem + w * 128, o = tmem + 256 + w * 128;
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
+              for (int part = 0; part < 2; ++part)
 #pragma unroll
-            for (int ks = 0; ks < kTcU / 16; ++ks)
-              tc_mma_ts(o, pa + (ks / 2) * 32 + part * 16 + (ks & 1) * 8,
-                        tc_desc(va + ks * 2048, C::kHalf), kIdPv, k >= 2 || part || ks);
-          tc_commit(pv_done + w);
-          tc_commit(v_empty + slot);
-          ++vg;
-          if (k + 2 < cnt) qk(w);
+                for (int ks = 0; ks < kTcU / 16; ++ks)
+                  tc_mma_ts(o, pa + (ks / 2) * 32 + part * 16 + (ks & 1) * 8,
+                            tc_desc(va + ks * 2048, C::kHalf), kIdPv, np >= 2 || part || ks);
+              tc_commit(pv_done + w);
+              tc_commit(v_empty + slot);
+              ++streams[w];
+              ++vg;
+              ++np;
+              idle = false;
+            }
+          }
+          if (nq < cnt && nq < np + 2) {
+            const int w = nq & 1, slot = kg % kTcStages;
+            if (mbar_test(k_full + slot, (kg / kTcStages) & 1)) {
+              tc_fence_after();
+              const uint32_t ka = smem_u32(smem + C::kOffK + slot * C::kTile);
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t o = (ks / 4) * C::kHalf + (ks % 4) * 32;
+                tc_mma_ss(tmem + w * 128, tc_desc(qa + o, 16), tc_desc(ka + o, 16), kIdQk, ks > 0);
+              }
+              tc_commit(s_full + w);
+              tc_commit(k_empty + slot);
+              ++kg;
+              ++nq;
+              idle = false;
+            }
+          }
+          if (!idle) {
+            t0 = globaltimer_ns();
+          } else if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            ok = false;
+            break;
+          }
         }
         u += cnt;
         if (cnt == left)
@@ -320,8 +343,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= 10) {
-    att_fill_padding<__nv_bfloat16>(p, 10, 2);
+  } else if (warp == 11) {
+    att_fill_padding<__nv_bfloat16>(p, 11, 1);
   } else {
     // ------------------------------- softmax -------------------------------
     const int w = warp >> 2, quad = warp & 3;
@@ -332,6 +355,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int tiles_done = 0;                           // of this warp group
     int tile_g = 0;                               // of the block
     bool dead = false;
+    constexpr int kPer = D / 16;                  // 16-byte pieces of half a row
+    uint4 qx[kPer];
+    auto load_q = [&](const AttCursor<kTcU, RT>& c) {
+      const int r = (tid & 127) % RT, qr = (c.seg % c.mt) * RT + r, h = c.seg / c.mt;
+      const bool on = qr < c.q * p.g;
+      const int i = on ? qr / p.g : 0, gi = on ? qr - i * p.g : 0;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const __nv_bfloat16*>(p.q) + c.b * p.q_b + i * p.q_t +
+          (long long)(h * p.g + gi) * D) + (tid >> 7) * kPer;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) qx[j] = on ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+    };
+    if (s.u0 < s.u1) load_q(cur);
     for (long long u = s.u0; u < s.u1;) {
       const int h = cur.seg / cur.mt, row0 = (cur.seg % cur.mt) * RT;
       const int rows = min(RT, cur.q * p.g - row0);
@@ -340,25 +376,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int kv = cur.kv, len = cur.kv + cur.q;
       const int32_t* par = p.parents ? p.parents + (long long)cur.b * p.n : nullptr;
       const int32_t* trow = p.table + (long long)cur.b * p.max_pages;
-      // the rows of q, and whether all pages are in the pool
-      {
-        const int r = tid & 127, hf = tid >> 7;
-        const int qr = row0 + r % RT;
-        const bool on = r % RT < rows;
-        const int i = on ? qr / p.g : 0, gi = on ? qr - i * p.g : 0;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(p.q) + cur.b * p.q_b + i * p.q_t +
-            (long long)(h * p.g + gi) * D) + hf * (D / 16);
-        constexpr int kPer = D / 16;  // 16-byte pieces of half a row
-        uint4 x[kPer];
+      // the rows of q: loaded while the last segment ended
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) x[j] = on ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int c = hf * kPer + j;
-          *reinterpret_cast<uint4*>(s_q + (c / 8) * C::kHalf + r * 128 +
-                                    (((c % 8) ^ (r & 7)) << 4)) = x[j];
-        }
+      for (int j = 0; j < kPer; ++j) {
+        const int c = (tid >> 7) * kPer + j, r = tid & 127;
+        *reinterpret_cast<uint4*>(s_q + (c / 8) * C::kHalf + r * 128 +
+                                  (((c % 8) ^ (r & 7)) << 4)) = qx[j];
       }
       // the pages of these tiles: loaded here, looked at when the tiles are done
       const int page0 = tile0 * kTcU / p.page;
@@ -512,6 +535,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ++tiles_done;
       }
       const bool used = w < cnt;
+      // where the next segment is, and its rows of q
+      AttCursor<kTcU, RT> next = cur;
+      if (cnt == left)
+        next.next_segment(p);
+      else
+        next.tile += cnt;
+      if (u + cnt < s.u1) load_q(next);
       if (used && !dead) {
         dead = !__all_sync(0xffffffffu, mbar_wait_bounded(pv_done + w, (tiles_done - 1) & 1));
         if (dead) *s_abort = 1;
@@ -662,10 +692,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (tid == 0) *s_bad = *s_fix = 0;
       softmax_sync();  // before the next segment's q and flags
       u += cnt;
-      if (tile0 + cnt == cur.tiles)
-        cur.next_segment(p);
-      else
-        cur.tile += cnt;
+      cur = next;
     }
     if (dead && lane == 0) kv_flag(p.status, SV_DEV_TIMEOUT);
   }
