@@ -103,30 +103,45 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
-__device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(a)
-      : "memory");
+__device__ __forceinline__ void tc_ld(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+               "%10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                 "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(a)
+               : "memory");
 }
-__device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31]), "r"(a)
-      : "memory");
+__device__ __forceinline__ void tc_st(uint32_t a, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, "
+               "%8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+               "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void tc_ld(uint32_t a, uint32_t (&r)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+               "%10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, "
+               "%26, %27, %28, %29, %30, %31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                 "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+                 "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                 "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+                 "=r"(r[30]), "=r"(r[31])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void tc_st(uint32_t a, const uint32_t (&r)[32]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, "
+               "%8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "
+               "%24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+               "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+               "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+               "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+               "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(a)
+               : "memory");
 }
 __device__ __forceinline__ void tc_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
@@ -283,7 +298,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // whichever product has its operands: S of tile nq (its warp group's
         // last P is used up), or P V of tile np
         int nq = 0, np = 0;
-        uint64_t t0 = globaltimer_ns();
+        uint64_t t0 = 0;  // the clock is far away: read once in many idle rounds
+        uint32_t spins = 0;
         while (np < cnt) {
           bool idle = true;
           if (np < nq) {
@@ -294,11 +310,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const uint32_t va = smem_u32(smem + C::kOffV + slot * C::kTile);
               const uint32_t pa = tmem + w * 128, o = tmem + 256 + w * 128;
 #pragma unroll
-              for (int part = 0; part < 2; ++part)
-#pragma unroll
-                for (int ks = 0; ks < kTcU / 16; ++ks)
-                  tc_mma_ts(o, pa + (ks / 2) * 32 + part * 16 + (ks & 1) * 8,
-                            tc_desc(va + ks * 2048, C::kHalf), kIdPv, np >= 2 || part || ks);
+              for (int ks = 0; ks < kTcU / 16; ++ks)
+                tc_mma_ts(o, pa + (ks / 2) * 32 + (ks & 1) * 8, tc_desc(va + ks * 2048, C::kHalf),
+                          kIdPv, np >= 2 || ks);
               tc_commit(pv_done + w);
               tc_commit(v_empty + slot);
               ++streams[w];
@@ -325,10 +339,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
           if (!idle) {
-            t0 = globaltimer_ns();
-          } else if (globaltimer_ns() - t0 > kWaitLimitNs) {
-            ok = false;
-            break;
+            spins = 0;
+          } else if ((++spins & 1023) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (spins == 1024) t0 = now;
+            if (now - t0 > kWaitLimitNs) {
+              ok = false;
+              break;
+            }
           }
         }
         u += cnt;
@@ -418,7 +436,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int c = 0; c < kKeys / 32; ++c) {
           uint32_t x[32];
-          tc_ld32(mine + c * 32, x);
+          tc_ld(mine + c * 32, x);
           tc_wait_ld();
           if (tail) {
 #pragma unroll
@@ -444,11 +462,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t y[32];
-            tc_ld32(o_at + c, y);
+            tc_ld(o_at + c, y);
             tc_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * a);
-            tc_st32(o_at + c, y);
+            tc_st(o_at + c, y);
           }
         }
         if (grow) {
@@ -458,19 +476,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float ms = m == -INFINITY ? 0.f : m;
         const unsigned long long cc = f2_pack(p.scale_log2, p.scale_log2), mm = f2_pack(-ms, -ms);
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        // P over S: the 32 columns of 32 keys take their bf16 pairs, first
-        // the first parts (16 columns), then the rests
+        // P over S: bf16 pairs in the first half of their keys' columns
 #pragma unroll
         for (int c = 0; c < kKeys / 32; ++c) {
           uint32_t x[32];
-          tc_ld32(mine + c * 32, x);
+          tc_ld(mine + c * 32, x);
           tc_wait_ld();
           if (tail) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!(seen[c] >> e & 1u)) x[e] = 0xff800000u;
           }
-          uint32_t y[32];
+          uint32_t y[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float a, b;
@@ -482,15 +499,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             sum[e & 1] += a;
             sum[2 + (e & 1)] += b;
             y[e] = pack_bf16(a, b);
-            y[16 + e] = pack_bf16(a - bf16_lo(y[e]), b - bf16_hi(y[e]));
           }
-          tc_st32(mine + c * 32, y);
+          tc_st(mine + c * 32, y);
         }
         if constexpr (kCopies > 1) {  // the other copies' keys
-          const uint32_t zero[32] = {};
+          const uint32_t zero[16] = {};
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (c / (kKeys / 32) != copy) tc_st32(s_at + c * 32, zero);
+            if (c / (kKeys / 32) != copy) tc_st(s_at + c * 32, zero);
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         if (tail) {
@@ -606,7 +622,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (used && !gone) {
           if constexpr (C::kCols == 32) {
             uint32_t y[32];
-            tc_ld32(o_at + c0, y);
+            tc_ld(o_at + c0, y);
             tc_wait_ld();
 #pragma unroll
             for (int j = 0; j < kPieces; ++j)
@@ -614,17 +630,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                   __uint_as_float(y[4 * j]) * f, __uint_as_float(y[4 * j + 1]) * f,
                   __uint_as_float(y[4 * j + 2]) * f, __uint_as_float(y[4 * j + 3]) * f);
           } else {
-            uint32_t y[32];
-            tc_ld32(o_at + (c0 & ~31), y);
+            uint32_t y[16];
+            tc_ld(o_at + c0, y);
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < kPieces; ++j) {
-              float z[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                z[e] = __uint_as_float(c0 & 16 ? y[16 + 4 * j + e] : y[4 * j + e]) * f;
-              dst[j ^ (lr & (kPieces - 1))] = make_float4(z[0], z[1], z[2], z[3]);
-            }
+            for (int j = 0; j < kPieces; ++j)
+              dst[j ^ (lr & (kPieces - 1))] = make_float4(
+                  __uint_as_float(y[4 * j]) * f, __uint_as_float(y[4 * j + 1]) * f,
+                  __uint_as_float(y[4 * j + 2]) * f, __uint_as_float(y[4 * j + 3]) * f);
           }
         } else {
 #pragma unroll
