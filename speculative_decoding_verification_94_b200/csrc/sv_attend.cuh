@@ -51,6 +51,7 @@ struct AttendParams {
   long long q_b, q_t;                 // strides of q, elements
   long long c_page, c_token, c_head;  // strides of the cache, elements
   float scale_log2;
+  FastDiv div_g, div_page;
   AttShared* shared;  // [grid] the shared segment that starts in block i
   float* partial;            // [grid][2] partial results
   int32_t* status;
@@ -78,31 +79,37 @@ __device__ __forceinline__ bool att_lens(const AttendParams& p, int b, int& kv, 
 }
 
 // The walk over units: requests, then segments (key head, row tile), then
-// tiles of U keys.
-template <int U, int RT>
+// tiles of U keys.  A segment counts OV units more than its tiles, which
+// stand before its first tile: what it costs to begin and end one, so that
+// blocks with many short segments get fewer tiles.
+template <int U, int RT, int OV>
 struct AttCursor {
   int b, seg, tile, tiles, mt, kv, q;
+  long long v;  // the tile's unit
   __device__ __forceinline__ long long load(const AttendParams& p) {  // units of request b
     tiles = mt = 0;
     if (b >= p.B || !att_lens(p, b, kv, q) || q == 0) return 0;
     tiles = (int)(((long long)kv + q + U - 1) / U);
     mt = (q * p.g + RT - 1) / RT;
-    return (long long)tiles * mt * p.hkv;
+    return (long long)(tiles + OV) * mt * p.hkv;
   }
-  __device__ __forceinline__ void place(long long off) {  // off: unit within the request
-    seg = (int)(off / tiles);
-    tile = (int)(off - (long long)seg * tiles);
+  __device__ __forceinline__ void place(long long unit, long long off) {  // off: in the request
+    seg = (int)(off / (tiles + OV));
+    const int r = (int)(off - (long long)seg * (tiles + OV)) - OV;
+    tile = r < 0 ? 0 : r;
+    v = unit + (tile - r);
   }
-  __device__ __forceinline__ void next_segment(const AttendParams& p) {
+  __device__ __forceinline__ void step(const AttendParams& p, int count) {  // within the segment
+    tile += count;
+    v += count;
+    if (tile < tiles) return;
+    v += OV;
     tile = 0;
     if (++seg == mt * p.hkv) {
       seg = 0;
       do ++b;
       while (b < p.B && load(p) == 0);
     }
-  }
-  __device__ __forceinline__ void advance(const AttendParams& p) {
-    if (++tile == tiles) next_segment(p);
   }
 };
 
@@ -118,8 +125,8 @@ struct AttShare {
 // Every block sums the units of all requests and finds its own run.  `scratch`
 // is kShareBytes of shared memory.
 constexpr int kShareBytes = 128;
-template <int U, int RT, int THREADS>
-__device__ __forceinline__ AttShare att_share(const AttendParams& p, AttCursor<U, RT>& cur,
+template <int THREADS, int U, int RT, int OV>
+__device__ __forceinline__ AttShare att_share(const AttendParams& p, AttCursor<U, RT, OV>& cur,
                                               void* scratch) {
   static_assert(8 * (THREADS / 32 + 2) <= kShareBytes, "");
   long long* s_sum = static_cast<long long*>(scratch);
@@ -167,10 +174,11 @@ __device__ __forceinline__ AttShare att_share(const AttendParams& p, AttCursor<U
     }
   }
   __syncthreads();
+  cur.v = s.u1;
   if (s.u0 < s.u1) {
     cur.b = s_b;
     cur.load(p);
-    cur.place(s_off);
+    cur.place(s.u0, s_off);
   }
   return s;
 }
@@ -221,7 +229,7 @@ __device__ __forceinline__ bool not_finite(float x) {
 
 // Output row of tile row r: token and query head.
 __device__ __forceinline__ long long att_out_row(const AttendParams& p, int b, int h, int r) {
-  const int i = r / p.g;
+  const int i = fast_div(r, p.div_g);
   return ((long long)b * p.n + i) * ((long long)p.hkv * p.g) + (long long)h * p.g + (r - i * p.g);
 }
 
@@ -381,7 +389,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendP
 // key and a warp four of the 16 rows while scores are formed, then a thread
 // holds a column of the output.
 // ---------------------------------------------------------------------------
-constexpr int kGenThreads = 128, kGenU = 32, kGenR = 16;
+constexpr int kGenThreads = 128, kGenU = 32, kGenR = 16, kGenOv = 1;
 
 template <int DP>
 struct GenSmem {
@@ -407,15 +415,15 @@ __global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const Atten
   const int col = tid % (kGenThreads / kRG), rg = tid / (kGenThreads / kRG) * kRows;
   if (tid == 0) att_clear_note(p);
   pdl_launch_dependents();
-  AttCursor<kGenU, kGenR> cur;
-  const AttShare s = att_share<kGenU, kGenR, kGenThreads>(p, cur, sm.share);
+  AttCursor<kGenU, kGenR, kGenOv> cur;
+  const AttShare s = att_share<kGenThreads>(p, cur, sm.share);
   const T* kc = static_cast<const T*>(p.k);
   const T* vc = static_cast<const T*>(p.v);
-  for (long long u = s.u0; u < s.u1;) {
+  while (cur.v < s.u1) {
     const int h = cur.seg / cur.mt, row0 = (cur.seg % cur.mt) * kGenR;
     const int rows = min(kGenR, cur.q * p.g - row0);
     const int tile0 = cur.tile, left = cur.tiles - cur.tile;
-    const int cnt = s.u1 - u < left ? (int)(s.u1 - u) : left;
+    const int cnt = s.u1 - cur.v < left ? (int)(s.u1 - cur.v) : left;
     const int len = cur.kv + cur.q;
     const int32_t* trow = p.table + (long long)cur.b * p.max_pages;
     const int32_t* par = p.parents ? p.parents + (long long)cur.b * p.n : nullptr;
@@ -425,7 +433,7 @@ __global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const Atten
       const int r = e / DP, d = e % DP;
       float x = 0.f;
       if (r < rows && d < p.d) {
-        const int i = (row0 + r) / p.g, gi = (row0 + r) - i * p.g;
+        const int i = fast_div(row0 + r, p.div_g), gi = (row0 + r) - i * p.g;
         x = to_f32<T>(static_cast<const T*>(p.q)[cur.b * p.q_b + i * p.q_t +
                                                  (long long)(h * p.g + gi) * p.d + d]);
       }
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const Atten
         const int pos = pos0 + tid;
         const unsigned char *rk = nullptr, *rv = nullptr;
         if (pos < len) {
-          const int pi = pos / p.page;
+          const int pi = fast_div(pos, p.div_page);
           const int id = trow[pi];
           if (id >= 0 && id < p.num_pages) {
             const long long at =
@@ -511,7 +519,7 @@ __global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const Atten
         const int r = warp + 4 * j;
         float x = z[j] * p.scale_log2;
         if (tail) {
-          const int i = min((row0 + r) / p.g, cur.q - 1);
+          const int i = min(fast_div(row0 + r, p.div_g), cur.q - 1);
           bool on = pos < cur.kv || (pos < len && pos - cur.kv <= i);
           if (par && pos0 + kGenU > cur.kv) {
             const int lo = pos0 - cur.kv;  // node of the tile's first key
@@ -611,13 +619,9 @@ __global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const Atten
         __stcg(t + kGenR * DP + kGenR + tid, bad ? nan : sm.l[tid]);
       }
       if (tid == 0 && tile0 == 0)
-        att_note(p, s, cur.b, h, row0, rows, u + cur.tiles);
+        att_note(p, s, cur.b, h, row0, rows, cur.v + cur.tiles);
     }
-    u += cnt;
-    if (tile0 + cnt == cur.tiles)
-      cur.next_segment(p);
-    else
-      cur.tile += cnt;
+    cur.step(p, cnt);
   }
   att_fill_padding<T>(p, 0, kGenThreads / 32);
 }

@@ -22,6 +22,7 @@
 
 namespace sv {
 
+constexpr int kMmaOv = 1;
 constexpr int kMmaThreads = 128, kMmaWarps = 4, kMmaKeys = 16, kMmaU = kMmaWarps * kMmaKeys;
 
 template <int D, int MT>
@@ -117,28 +118,28 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
 
   if (tid == 0) att_clear_note(p);
   pdl_launch_dependents();
-  AttCursor<kMmaU, kRows> cur;
-  const AttShare s = att_share<kMmaU, kRows, kMmaThreads>(p, cur, merge);
+  AttCursor<kMmaU, kRows, kMmaOv> cur;
+  const AttShare s = att_share<kMmaThreads>(p, cur, merge);
 
   // ---- the copies: they run kStages - 1 tiles ahead of the products ---------
-  AttCursor<kMmaU, kRows> ahead = cur;
-  long long ua = s.u0;
+  AttCursor<kMmaU, kRows, kMmaOv> ahead = cur;
   uint32_t bad_stages = 0;
   // page of this lane's key in the tile to be copied next; -1: past the end
   auto page_of = [&]() {
     const int pos = ahead.tile * kMmaU + warp * kMmaKeys + (lane & 15);
-    if (ua >= s.u1 || pos >= ahead.kv + ahead.q) return -1;
-    const int id = __ldg(p.table + (long long)ahead.b * p.max_pages + pos / p.page);
+    if (ahead.v >= s.u1 || pos >= ahead.kv + ahead.q) return -1;
+    const int id = __ldg(p.table + (long long)ahead.b * p.max_pages + fast_div(pos, p.div_page));
     return id >= 0 && id < p.num_pages ? id : -2;
   };
   int page = page_of();
   auto copy_next = [&](int stage) {
-    if (ua < s.u1) {
+    if (ahead.v < s.u1) {
       const int h = ahead.seg / ahead.mt;
       const int pos = ahead.tile * kMmaU + warp * kMmaKeys + (lane & 15);
       long long at = -1;
       if (page >= 0)
-        at = page * p.c_page + (long long)(pos % p.page) * p.c_token + h * p.c_head;
+        at = page * p.c_page +
+             (long long)(pos - fast_div(pos, p.div_page) * p.page) * p.c_token + h * p.c_head;
       const bool bad = __any_sync(0xffffffffu, page == -2);
       bad_stages = (bad_stages & ~(1u << stage)) | ((uint32_t)bad << stage);
       const uint32_t dst = smem_u32(ring + stage * C::kStage);
@@ -153,8 +154,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
         cp_async16(to, kc + src, on);
         cp_async16(to + C::kPlane, vc + src, on);
       }
-      ++ua;
-      ahead.advance(p);
+      ahead.step(p, 1);
       page = page_of();
     }
     cp_async_commit();
@@ -163,11 +163,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
   for (int j = 0; j < kStages - 1; ++j) copy_next(j);
   int stage = 0;
 
-  for (long long u = s.u0; u < s.u1;) {
+  while (cur.v < s.u1) {
     const int h = cur.seg / cur.mt, row0 = (cur.seg % cur.mt) * kRows;
     const int rows = min(kRows, cur.q * p.g - row0);
     const int tile0 = cur.tile, left = cur.tiles - cur.tile;
-    const int cnt = s.u1 - u < left ? (int)(s.u1 - u) : left;
+    const int cnt = s.u1 - cur.v < left ? (int)(s.u1 - cur.v) : left;
     const int kv = cur.kv, len = cur.kv + cur.q;
     const int32_t* par = p.parents ? p.parents + (long long)cur.b * p.n : nullptr;
 
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
       for (int half = 0; half < 2; ++half) {
         const int r = row0 + mt * 16 + half * 8 + (lane >> 2);
         const bool on = r - row0 < rows;
-        const int i = on ? r / p.g : 0, gi = on ? r - i * p.g : 0;
+        const int i = on ? fast_div(r, p.div_g) : 0, gi = on ? r - i * p.g : 0;
         const uint32_t* src = reinterpret_cast<const uint32_t*>(
             static_cast<const __nv_bfloat16*>(p.q) + cur.b * p.q_b + i * p.q_t +
             (long long)(h * p.g + gi) * D + (lane & 3) * 2);
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
           seen[mt][half] = 0xffffu;
           if (tail) {
             const int r = row0 + mt * 16 + half * 8 + (lane >> 2);
-            const int i = min(r / p.g, cur.q - 1);
+            const int i = min(fast_div(r, p.div_g), cur.q - 1);
             const uint32_t bits = att_tail_bits<kMmaKeys>(par, i, pos0, kv, tree_ok);
             seen[mt][half] = bits;
 #pragma unroll
@@ -447,13 +447,9 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
       }
     }
     if (!whole && tile0 == 0 && tid == 0)
-      att_note(p, s, cur.b, h, row0, rows, u + cur.tiles);
+      att_note(p, s, cur.b, h, row0, rows, cur.v + cur.tiles);
     __syncthreads();  // merge is free again
-    u += cnt;
-    if (tile0 + cnt == cur.tiles)
-      cur.next_segment(p);
-    else
-      cur.tile += cnt;
+    cur.step(p, cnt);
   }
   cp_async_wait<0>();
   att_fill_padding<__nv_bfloat16>(p, 0, kMmaWarps);

@@ -34,6 +34,7 @@
 namespace sv {
 
 constexpr int kTcU = 128;            // keys of a tile
+constexpr int kTcOv = 3;             // a segment's beginning and end, in tiles: about 5 us
 constexpr int kTcSoftmax = 256;      // threads of the two warp groups
 constexpr int kTcThreads = 384;      // + two copy warps, product warp, one for the rest
 constexpr int kTcStages = 3;
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t *k_full = bars, *k_empty = bars + 3, *v_full = bars + 6, *v_empty = bars + 9,
-           *s_full = bars + 12, *p_ready = bars + 14, *pv_done = bars + 16, *q_full = bars + 18;
+           *s_full = bars + 12, *p_ready = bars + 14, *pv_done = bars + 16, *q_full = bars + 18, *q_first = bars + 19;
   int* misc = reinterpret_cast<int*>(smem + C::kOffMisc);
   volatile int* s_abort = misc;      // a wait ran out
   int* s_bad = misc + 1;             // the segment's keys are on a bad page
@@ -215,6 +216,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(pv_done + i, 1);
     }
     mbar_init(q_full, kTcSoftmax);
+    mbar_init(q_first, kTcSoftmax);
     fence_mbar_init();
     misc[0] = misc[1] = misc[2] = 0;
     att_clear_note(p);
@@ -227,8 +229,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_before();
   }
   pdl_launch_dependents();
-  AttCursor<kTcU, RT> cur;
-  const AttShare s = att_share<kTcU, RT, kTcThreads>(p, cur, smem + C::kOffShare);
+  AttCursor<kTcU, RT, kTcOv> cur;
+  const AttShare s = att_share<kTcThreads>(p, cur, smem + C::kOffShare);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
@@ -243,24 +245,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const bool mine = bi < boxes && half < kHalves;
     uint64_t *fulls = keys ? k_full : v_full, *empties = keys ? k_empty : v_empty;
     unsigned char* ring = smem + (keys ? C::kOffK : C::kOffV) + half * C::kHalf + bi * tp.box * 128;
-    long long u = s.u0;
     auto page_of = [&]() {  // out of the pool: zeros are copied
       const int pos = cur.tile * kTcU + bi * tp.box;
-      if (u >= s.u1 || !mine || pos >= cur.kv + cur.q) return p.num_pages;
-      const int id = __ldg(p.table + (long long)cur.b * p.max_pages + pos / p.page);
+      if (cur.v >= s.u1 || !mine || pos >= cur.kv + cur.q) return p.num_pages;
+      const int id = __ldg(p.table + (long long)cur.b * p.max_pages + fast_div(pos, p.div_page));
       return id >= 0 && id < p.num_pages ? id : p.num_pages;
     };
     int page = page_of();
     int slot = 0, round = 0;
     bool ok = true;
-    while (u < s.u1) {
+    while (cur.v < s.u1) {
       const int h = cur.seg / cur.mt;
-      const int token = (cur.tile * kTcU + bi * tp.box) % p.page;
+      const int pos = cur.tile * kTcU + bi * tp.box;
+      const int token = pos - fast_div(pos, p.div_page) * p.page;
       const int id = page;
-      ++u;
-      cur.advance(p);
+      cur.step(p, 1);
       page = page_of();
       if (round) ok = __all_sync(0xffffffffu, mbar_wait_bounded(empties + slot, (round - 1) & 1));
+      // q is on its way with the first tile; the others would come before it
+      if (slot == 1 && round == 0)
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(q_first, 0));
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(fulls + slot, C::kTile);
       __syncwarp();
@@ -288,9 +292,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int streams[2] = {0, 0};  // tiles of each warp group
       int segs = 0;
       bool ok = true;
-      for (long long u = s.u0; u < s.u1 && ok;) {
+      while (cur.v < s.u1 && ok) {
         const int left = cur.tiles - cur.tile;
-        const int cnt = s.u1 - u < left ? (int)(s.u1 - u) : left;
+        const int cnt = s.u1 - cur.v < left ? (int)(s.u1 - cur.v) : left;
         ok = mbar_wait_bounded(q_full, segs & 1);
         ++segs;
         if (!ok) break;
@@ -349,11 +353,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
         }
-        u += cnt;
-        if (cnt == left)
-          cur.next_segment(p);
-        else
-          cur.tile += cnt;
+        cur.step(p, cnt);
       }
       if (!ok) {
         *s_abort = 1;
@@ -373,43 +373,51 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int tiles_done = 0;                           // of this warp group
     int tile_g = 0;                               // of the block
     bool dead = false;
-    constexpr int kPer = D / 16;                  // 16-byte pieces of half a row
+    // q: neighbouring threads load neighbouring 16 bytes; a row goes to each of
+    // its copies
+    constexpr int kPieces16 = D / 8, kPer = RT * kPieces16 / kTcSoftmax;
     uint4 qx[kPer];
-    auto load_q = [&](const AttCursor<kTcU, RT>& c) {
-      const int r = (tid & 127) % RT, qr = (c.seg % c.mt) * RT + r, h = c.seg / c.mt;
-      const bool on = qr < c.q * p.g;
-      const int i = on ? qr / p.g : 0, gi = on ? qr - i * p.g : 0;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          static_cast<const __nv_bfloat16*>(p.q) + c.b * p.q_b + i * p.q_t +
-          (long long)(h * p.g + gi) * D) + (tid >> 7) * kPer;
+    auto load_q = [&](const AttCursor<kTcU, RT, kTcOv>& c) {
+      const int h = c.seg / c.mt, first = (c.seg - h * c.mt) * RT;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) qx[j] = on ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < kPer; ++j) {
+        const int qr = first + (tid + j * kTcSoftmax) / kPieces16;
+        const bool on = qr < c.q * p.g;
+        const int i = on ? fast_div(qr, p.div_g) : 0, gi = on ? qr - i * p.g : 0;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(p.q) + c.b * p.q_b + i * p.q_t +
+            (long long)(h * p.g + gi) * D);
+        qx[j] = on ? __ldg(src + tid % kPieces16) : make_uint4(0, 0, 0, 0);
+      }
     };
-    if (s.u0 < s.u1) load_q(cur);
-    for (long long u = s.u0; u < s.u1;) {
+    if (cur.v < s.u1) load_q(cur);
+    while (cur.v < s.u1) {
       const int h = cur.seg / cur.mt, row0 = (cur.seg % cur.mt) * RT;
       const int rows = min(RT, cur.q * p.g - row0);
       const int tile0 = cur.tile, left = cur.tiles - cur.tile;
-      const int cnt = s.u1 - u < left ? (int)(s.u1 - u) : left;
+      const int cnt = s.u1 - cur.v < left ? (int)(s.u1 - cur.v) : left;
       const int kv = cur.kv, len = cur.kv + cur.q;
       const int32_t* par = p.parents ? p.parents + (long long)cur.b * p.n : nullptr;
       const int32_t* trow = p.table + (long long)cur.b * p.max_pages;
       // the rows of q: loaded while the last segment ended
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const int c = (tid >> 7) * kPer + j, r = tid & 127;
-        *reinterpret_cast<uint4*>(s_q + (c / 8) * C::kHalf + r * 128 +
-                                  (((c % 8) ^ (r & 7)) << 4)) = qx[j];
+        const int c = tid % kPieces16, r = (tid + j * kTcSoftmax) / kPieces16;
+#pragma unroll
+        for (int copy = 0; copy < kCopies; ++copy)  // RT is a multiple of the 8 rows of an atom
+          *reinterpret_cast<uint4*>(s_q + (c / 8) * C::kHalf + (copy * RT + r) * 128 +
+                                    (((c % 8) ^ (r & 7)) << 4)) = qx[j];
       }
       // the pages of these tiles: loaded here, looked at when the tiles are done
-      const int page0 = tile0 * kTcU / p.page;
-      const int pages = (min((tile0 + cnt) * kTcU, len) - 1) / p.page + 1 - page0;
+      const int page0 = fast_div(tile0 * kTcU, p.div_page);
+      const int pages = fast_div(min((tile0 + cnt) * kTcU, len) - 1, p.div_page) + 1 - page0;
       const int id0 = tid < pages ? __ldg(trow + page0 + tid) : 0;
       const int id1 = tid + kTcSoftmax < pages ? __ldg(trow + page0 + tid + kTcSoftmax) : 0;
       fence_async_smem();
       tc_fence_before();
       mbar_arrive(q_full);
-      const int qi = min((row0 + row) / p.g, cur.q - 1);
+      if (tile_g == 0) mbar_arrive(q_first);
+      const int qi = min(fast_div(row0 + row, p.div_g), cur.q - 1);
       float m = -INFINITY, l = 0.f;
       bool tree_ok = true;
       for (int k = w; k < cnt; k += 2) {
@@ -552,12 +560,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       const bool used = w < cnt;
       // where the next segment is, and its rows of q
-      AttCursor<kTcU, RT> next = cur;
-      if (cnt == left)
-        next.next_segment(p);
-      else
-        next.tile += cnt;
-      if (u + cnt < s.u1) load_q(next);
+      AttCursor<kTcU, RT, kTcOv> next = cur;
+      next.step(p, cnt);
+      if (next.v < s.u1) load_q(next);
       if (used && !dead) {
         dead = !__all_sync(0xffffffffu, mbar_wait_bounded(pv_done + w, (tiles_done - 1) & 1));
         if (dead) *s_abort = 1;
@@ -659,7 +664,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int col = c0 + j * 4;
           if (fix) {
             float* av = &a.x;
-            const int i = (row0 + r) / p.g;
+            const int i = fast_div(row0 + r, p.div_g);
             for (int t = max(0, tile0 * kTcU - kv); t < cur.q; ++t) {
               const int pos = kv + t;
               if (pos >= (tile0 + cnt) * kTcU) break;
@@ -700,11 +705,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       if (!whole && tile0 == 0 && tid == 0)
-        att_note(p, s, cur.b, h, row0, rows, u + cur.tiles);
+        att_note(p, s, cur.b, h, row0, rows, cur.v + cur.tiles);
       tc_fence_before();
       if (tid == 0) *s_bad = *s_fix = 0;
       softmax_sync();  // before the next segment's q and flags
-      u += cnt;
       cur = next;
     }
     if (dead && lane == 0) kv_flag(p.status, SV_DEV_TIMEOUT);

@@ -363,6 +363,8 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_st
   p.c_page = cache->page_stride;
   p.c_token = cache->token_stride;
   p.c_head = cache->head_stride;
+  p.div_g = make_fastdiv(p.g);
+  p.div_page = make_fastdiv(p.page);
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.shared = static_cast<AttShared*>(scratch);
   p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + kSharedBytes);
