@@ -80,6 +80,8 @@ def lib_path() -> Path:
 def lib() -> ctypes.CDLL:
     """Load libsv.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not _LIB_PATH.exists():
@@ -551,22 +553,51 @@ def sv_kd_grad(topk_logp: torch.Tensor, topk_idx: torch.Tensor, draft: torch.Ten
 # ---------------------------------------------------------------------------
 # The paged key-value cache of a verification step
 # ---------------------------------------------------------------------------
-def _on(dev: torch.device, stream):
-    """Context of a call: `dev` is the current device, which the C calls use,
-    and `stream`, if given, the stream of what the binding allocates."""
-    return torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream)
+def _launch(fn, what: str, dev: torch.device, stream, *args) -> None:
+    """Calls the C function on `stream` (None: the current one of `dev`) with
+    `dev` as the current device."""
+    idx = dev.index
+    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(idx)
+    if torch._C._cuda_getDevice() == idx:
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc != SV_OK:
+        raise SVError(what, rc)
 
 
-def _ptr(t, name: str, dtype, dev, numel: int | None = None):
-    """Data pointer of a dense device tensor (None stays None), checked."""
+def _empty(shape, dtype, dev, stream):
+    """Device memory that belongs to the stream of the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _ptr(t, name: str, dtype, dev, numel: int):
+    """Data pointer of a dense device tensor of `numel` entries (None stays
+    None), checked."""
     if t is None:
         return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and \
+            t.is_contiguous() and t.numel() == numel:
+        return t.data_ptr()
     _dev(t, name, dtype)
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}")
-    if numel is not None and t.numel() != numel:
-        raise ValueError(f"{name} must have {numel} entries, got {t.numel()}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must have {numel} entries, got {t.numel()}")
+
+
+def _rows(t, name: str, dev, B: int) -> tuple[int, int]:
+    """Data pointer and width of a dense int32 matrix of B rows."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == dev and \
+            t.is_contiguous() and t.dim() == 2 and t.shape[0] == B:
+        return t.data_ptr(), t.shape[1]
+    _dev(t, name, torch.int32)
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    raise ValueError(f"{name} must be a matrix of {B} rows")
 
 
 def _kv_cache(k: torch.Tensor, v: torch.Tensor) -> sv_kv_cache:
@@ -575,27 +606,30 @@ def _kv_cache(k: torch.Tensor, v: torch.Tensor) -> sv_kv_cache:
     for t, name in ((k, "k_cache"), (v, "v_cache")):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+    shape, st = k.shape, k.stride()
+    if len(shape) != 4 or shape != v.shape or k.dtype != v.dtype or k.device != v.device:
         raise ValueError("k_cache and v_cache must be [num_pages, page_size, heads, head_dim] of "
                          "one shape, type and device")
-    if k.stride() != v.stride() or (k.stride(3) != 1 and k.shape[3] > 1):
+    if st != v.stride() or (st[3] != 1 and shape[3] > 1):
         raise ValueError("k_cache and v_cache must have the same strides and dense rows")
-    return sv_kv_cache(k.data_ptr(), v.data_ptr(), _dtype_code(k), *k.shape, *k.stride()[:3])
+    return sv_kv_cache(k.data_ptr(), v.data_ptr(), _dtype_code(k), *shape, *st[:3])
 
 
 def _token_rows(t: torch.Tensor, name: str, cache: torch.Tensor, heads: int | None):
-    """Batch and token strides of [B, n, heads, head_dim] with dense tokens."""
+    """Shape, batch stride and token stride of [B, n, heads, head_dim] with
+    dense tokens."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != 4 or t.shape[3] != cache.shape[-1] or (heads and t.shape[2] != heads):
+    shape = t.shape
+    if len(shape) != 4 or shape[3] != cache.shape[-1] or (heads and shape[2] != heads):
         raise ValueError(f"{name} must be [B, n, heads, head_dim] matching the cache, got "
-                         f"{tuple(t.shape)}")
+                         f"{tuple(shape)}")
     if t.dtype != cache.dtype or t.device != cache.device:
         raise ValueError(f"{name} must have the cache's type and device")
-    d = t.shape[3]
-    if (d > 1 and t.stride(3) != 1) or (t.shape[2] > 1 and t.stride(2) != d):
+    st = t.stride()
+    if (shape[3] > 1 and st[3] != 1) or (shape[2] > 1 and st[2] != shape[3]):
         raise ValueError(f"the heads of a token of {name} must be dense")
-    return t.stride(0), t.stride(1)
+    return shape, st[0], st[1]
 
 
 def sv_kv_plan(kv_len: torch.Tensor, block_table: torch.Tensor, pages: torch.Tensor,
@@ -611,31 +645,29 @@ def sv_kv_plan(kv_len: torch.Tensor, block_table: torch.Tensor, pages: torch.Ten
     _dev(kv_len, "kv_len", torch.int32)
     dev = kv_len.device
     B, i32 = kv_len.numel(), torch.int32
-    _dev(block_table, "block_table", i32)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must be [{B}, max_pages]")
     o = dict(out) if out else {}
-    with _on(dev, stream):
+    if len(o) < 6:
         for name, shape, dt in (("kv_len", (B,), i32), ("pages", (B,), i32),
                                 ("free_count", (1,), i32), ("q_len", (B,), i32),
                                 ("slot_map", (B, max_new), torch.int64),
                                 ("positions", (B, max_new), i32)):
             if name not in o:
-                o[name] = torch.empty(shape, dtype=dt, device=dev)
-    args = (kv_len.data_ptr(), _ptr(written, "written", i32, dev, B),
-            _ptr(accepted_len, "accepted_len", i32, dev, B), _ptr(release, "release", i32, dev, B),
-            _ptr(new_len, "new_len", i32, dev, B), B, int(max_new), int(page_size),
-            free_pages.numel(), _ptr(block_table, "block_table", i32, dev), block_table.shape[1],
-            _ptr(pages, "pages", i32, dev, B), _ptr(free_pages, "free_pages", i32, dev),
+                o[name] = _empty(shape, dt, dev, stream)
+    table, max_pages = _rows(block_table, "block_table", dev, B)
+    _dev(free_pages, "free_pages", i32)
+    num = free_pages.numel()
+    _launch(lib().sv_kv_plan, "sv_kv_plan", dev, stream, kv_len.data_ptr(),
+            _ptr(written, "written", i32, dev, B), _ptr(accepted_len, "accepted_len", i32, dev, B),
+            _ptr(release, "release", i32, dev, B), _ptr(new_len, "new_len", i32, dev, B), B,
+            max_new, page_size, num, table, max_pages, _ptr(pages, "pages", i32, dev, B),
+            _ptr(free_pages, "free_pages", i32, dev, num),
             _ptr(free_count, "free_count", i32, dev, 1), _ptr(o["kv_len"], "kv_len", i32, dev, B),
             _ptr(o["pages"], "pages", i32, dev, B),
             _ptr(o["free_count"], "free_count", i32, dev, 1),
             _ptr(o["q_len"], "q_len", i32, dev, B),
             _ptr(o["slot_map"], "slot_map", torch.int64, dev, B * max_new),
             _ptr(o["positions"], "positions", i32, dev, B * max_new),
-            _ptr(device_status, "device_status", i32, dev))
-    with _on(dev, stream):
-        _check(lib().sv_kv_plan(*args, _stream(dev, stream)), "sv_kv_plan")
+            _ptr(device_status, "device_status", i32, dev, 1))
     return o
 
 
@@ -647,15 +679,13 @@ def sv_kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cac
     page_size, heads, head_dim] (see sv.h)."""
     c = _kv_cache(k_cache, v_cache)
     dev = k_cache.device
-    st = _token_rows(k, "k", k_cache, k_cache.shape[2])
-    if _token_rows(v, "v", k_cache, k_cache.shape[2]) != st or v.shape != k.shape:
+    rows = _token_rows(k, "k", k_cache, c.heads)
+    if _token_rows(v, "v", k_cache, c.heads) != rows:
         raise ValueError("k and v must have the same shape and strides")
-    B, n = k.shape[:2]
-    args = (ctypes.byref(c), k.data_ptr(), v.data_ptr(), B, n, st[0], st[1],
-            _ptr(slot_map, "slot_map", torch.int64, dev, B * n),
-            _ptr(device_status, "device_status", torch.int32, dev))
-    with _on(dev, stream):
-        _check(lib().sv_kv_append(*args, _stream(dev, stream)), "sv_kv_append")
+    (B, n, _, _), sb, st = rows
+    _launch(lib().sv_kv_append, "sv_kv_append", dev, stream, ctypes.byref(c), k.data_ptr(),
+            v.data_ptr(), B, n, sb, st, _ptr(slot_map, "slot_map", torch.int64, dev, B * n),
+            _ptr(device_status, "device_status", torch.int32, dev, 1))
 
 
 def sv_kv_attend_scratch_size(B: int, n: int, q_heads: int, heads: int, head_dim: int,
@@ -677,30 +707,24 @@ def sv_kv_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     (torch's allocator gives them if it is None)."""
     c = _kv_cache(k_cache, v_cache)
     dev, i32 = k_cache.device, torch.int32
-    st = _token_rows(q, "q", k_cache, None)
-    B, n, hq, d = q.shape
-    _dev(block_table, "block_table", i32)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must be [{B}, max_pages]")
+    (B, n, hq, d), sb, st = _token_rows(q, "q", k_cache, None)
     o = dict(out) if out else {}
-    with _on(dev, stream):
-        if "out" not in o:
-            o["out"] = torch.empty(B, n, hq, d, dtype=q.dtype, device=dev)
-        if "lse" not in o:
-            o["lse"] = torch.empty(B, n, hq, dtype=torch.float32, device=dev)
-        if scratch is None:
-            nbytes = lib().sv_kv_attend_scratch_size(B, n, hq, k_cache.shape[2], d, c.dtype)
-            scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _check(lib().sv_kv_attend(
-            ctypes.byref(c), q.data_ptr(), st[0], st[1], B, n, hq,
-            _ptr(block_table, "block_table", i32, dev), block_table.shape[1],
-            _ptr(kv_len, "kv_len", i32, dev, B), _ptr(q_len, "q_len", i32, dev, B),
-            _ptr(parents, "parents", i32, dev, B * n),
-            float(d ** -0.5 if scale is None else scale),
-            _ptr(o["out"], "out", q.dtype, dev, q.numel()),
+    if "out" not in o:
+        o["out"] = _empty((B, n, hq, d), q.dtype, dev, stream)
+    if "lse" not in o:
+        o["lse"] = _empty((B, n, hq), torch.float32, dev, stream)
+    L = lib()
+    if scratch is None:
+        scratch = _empty(L.sv_kv_attend_scratch_size(B, n, hq, c.heads, d, c.dtype), torch.uint8,
+                         dev, stream)
+    table, max_pages = _rows(block_table, "block_table", dev, B)
+    _launch(L.sv_kv_attend, "sv_kv_attend", dev, stream, ctypes.byref(c), q.data_ptr(), sb, st, B,
+            n, hq, table, max_pages, _ptr(kv_len, "kv_len", i32, dev, B),
+            _ptr(q_len, "q_len", i32, dev, B), _ptr(parents, "parents", i32, dev, B * n),
+            d ** -0.5 if scale is None else scale, _ptr(o["out"], "out", q.dtype, dev, B * n * hq * d),
             _ptr(o["lse"], "lse", torch.float32, dev, B * n * hq),
-            _ptr(scratch, "scratch", torch.uint8, dev), scratch.numel(),
-            _ptr(device_status, "device_status", i32, dev), _stream(dev, stream)), "sv_kv_attend")
+            _ptr(scratch, "scratch", torch.uint8, dev, scratch.numel()), scratch.numel(),
+            _ptr(device_status, "device_status", i32, dev, 1))
     return o
 
 
@@ -723,16 +747,11 @@ def sv_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torc
         k0, v0 = k_cache[0], v_cache[0]
     c = _kv_cache(k0, v0)
     dev, i32 = k0.device, torch.int32
+    _dev(kv_len, "kv_len", i32)
     B = kv_len.numel()
-    for t, name in ((block_table, "block_table"), (accepted_nodes, "accepted_nodes")):
-        _dev(t, name, i32)
-        if t.dim() != 2 or t.shape[0] != B:
-            raise ValueError(f"{name} must be a matrix of {B} rows")
-    args = (ctypes.byref(c), layers, layer_stride, B,
-            _ptr(block_table, "block_table", i32, dev), block_table.shape[1],
-            _ptr(kv_len, "kv_len", i32, dev, B),
-            _ptr(accepted_nodes, "accepted_nodes", i32, dev), accepted_nodes.shape[1],
+    table, max_pages = _rows(block_table, "block_table", dev, B)
+    nodes, width = _rows(accepted_nodes, "accepted_nodes", dev, B)
+    _launch(lib().sv_kv_commit, "sv_kv_commit", dev, stream, ctypes.byref(c), layers, layer_stride,
+            B, table, max_pages, _ptr(kv_len, "kv_len", i32, dev, B), nodes, width,
             _ptr(accepted_len, "accepted_len", i32, dev, B),
-            _ptr(device_status, "device_status", i32, dev))
-    with _on(dev, stream):
-        _check(lib().sv_kv_commit(*args, _stream(dev, stream)), "sv_kv_commit")
+            _ptr(device_status, "device_status", i32, dev, 1))
