@@ -291,7 +291,7 @@ __device__ __forceinline__ void att_clear_note(const AttendParams& p) {
 constexpr int kJoinThreads = 128;
 template <class T, int DP, int RT>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendParams p) {
-  constexpr int kSplit = RT >= 128 ? 1 : RT == 64 ? 2 : 4;
+  constexpr int kSplit = RT >= 128 ? 1 : RT == 64 ? 2 : 4;  // RT 4 to 32: 4
   constexpr int kRowsHere = 4 / kSplit;
   constexpr int kV = DP / 32;  // values of a lane
   constexpr int kBatch = 8;

@@ -6,6 +6,7 @@
 #include <initializer_list>
 
 #include "sv_attend.cuh"
+#include "sv_attend_f32.cuh"
 #include "sv_attend_mma.cuh"
 #include "sv_attend_tc.cuh"
 #include "sv_kv_pages.cuh"
@@ -207,6 +208,19 @@ cudaError_t launch_mma(AttendParams& p, cudaStream_t s) {
                                              MmaCfg<D, 2>::kSmem, s);
 }
 
+template <int D>
+cudaError_t launch_f32(AttendParams& p, cudaStream_t s) {
+  const int rows = p.n * p.g;
+  if (rows <= 4)
+    return launch_attend<float, D, 4>(attend_f32_kernel<D, 4>, p, kF32Threads, F32Cfg<D, 4>::kSmem,
+                                      s);
+  if (rows <= 8)
+    return launch_attend<float, D, 8>(attend_f32_kernel<D, 8>, p, kF32Threads, F32Cfg<D, 8>::kSmem,
+                                      s);
+  return launch_attend<float, D, 16>(attend_f32_kernel<D, 16>, p, kF32Threads,
+                                     F32Cfg<D, 16>::kSmem, s);
+}
+
 }  // namespace
 }  // namespace sv
 
@@ -388,6 +402,8 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_st
     e = launch_mma<128>(p, s);
   else if (cache->dtype == SV_BF16 && vec && pairs && p.d == 64)
     e = launch_mma<64>(p, s);
+  else if (cache->dtype == SV_F32 && vec && aligned(out, 16) && (p.d == 64 || p.d == 128))
+    e = p.d == 128 ? launch_f32<128>(p, s) : launch_f32<64>(p, s);
   else if (cache->dtype == SV_BF16)
     e = vec ? launch_general<__nv_bfloat16, true>(p, s) : launch_general<__nv_bfloat16, false>(p, s);
   else
