@@ -64,6 +64,24 @@ cudaError_t launch(K kernel, const Prm& prm, dim3 grid, int threads, int smem, c
   return launch_mark_after(s, cudaGetLastError());
 }
 
+// A launch that follows another of the same call: its blocks may be on the
+// device before the first ends; the kernel waits for it.
+template <class K, class Prm>
+cudaError_t launch_after(K kernel, const Prm& prm, dim3 grid, int threads, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = launch_mark_before(s);
+  if (e != cudaSuccess) return e;
+  return launch_mark_after(s, cudaLaunchKernelEx(&cfg, kernel, prm));
+}
+
 // ---------------------------------------------------------------------------
 // Attention: grid and scratch
 // ---------------------------------------------------------------------------
@@ -84,23 +102,14 @@ size_t attend_scratch(int rows, int head_dim, sv_dtype dt) {
                              4;
 }
 
-// The second launch: its blocks are on the device before the first ends.
+// The second launch.
 template <class T, int DP, int RT>
 cudaError_t launch_join(const AttendParams& p, int grid, cudaStream_t s) {
   constexpr int kRowsHere = RT >= 128 ? 4 : RT == 64 ? 2 : 1;
   const int rows = std::min(RT, p.n * p.g);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)((rows + kRowsHere - 1) / kRowsHere));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = launch_mark_before(s);
-  if (e != cudaSuccess) return e;
-  return launch_mark_after(s, cudaLaunchKernelEx(&cfg, attend_join_kernel<T, DP, RT>, p));
+  return launch_after(attend_join_kernel<T, DP, RT>, p,
+                      dim3((unsigned)grid, (unsigned)((rows + kRowsHere - 1) / kRowsHere)),
+                      kJoinThreads, s);
 }
 
 template <class T, int DP, int RT, class K>
@@ -256,19 +265,42 @@ sv_status sv_kv_plan(const int32_t* kv_len, const int32_t* written, const int32_
   if (B > kPlanMaxB || (long long)B * max_pages > 0x7fffffffLL ||
       (long long)B * max_new > 0x7fffffffLL)
     return SV_ERR_UNSUPPORTED;
-  const PlanParams p = {kv_len, written,   accepted_len, release,    new_len,   pages,
-                        free_count, B,     max_new,      page_size,  num_pages, max_pages,
-                        block_table, free_pages, kv_len_out, pages_out, free_count_out, q_len,
-                        slot_map, positions, device_status,
-                        (long long)B * max_new <= kPlanInlineSlots};
+  if (page_size > (1 << 30) || max_new > (1 << 30)) return SV_ERR_UNSUPPORTED;
+  PlanParams p = {};
+  p.kv_len = kv_len;
+  p.written = written;
+  p.accepted = accepted_len;
+  p.release = release;
+  p.new_len = new_len;
+  p.pages = pages;
+  p.free_count = free_count;
+  p.B = B;
+  p.max_new = max_new;
+  p.page = page_size;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages;
+  p.div_page = make_fastdiv(page_size);
+  p.div_new = make_fastdiv(max_new);
+  p.table = block_table;
+  p.free_pages = free_pages;
+  p.kv_len_out = kv_len_out;
+  p.pages_out = pages_out;
+  p.free_count_out = free_count_out;
+  p.q_len = q_len;
+  p.slot_map = slot_map;
+  p.positions = positions;
+  p.status = device_status;
+  const long long slots = (long long)B * max_new;
+  p.write_slots = slots <= kPlanInlineSlots;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch(kv_plan_kernel, p, dim3(1), kPlanThreads, (int)plan_smem(B), s);
+  cudaError_t e = launch(kv_plan_kernel, p, dim3(1), plan_threads(B, slots),
+                         (int)plan_smem(B), s);
   if (e != cudaSuccess) return SV_ERR_CUDA;
   if (!p.write_slots) {
     constexpr int kPerBlock = kSlotThreads * kSlotPer;
-    e = launch(kv_plan_slots_kernel, p,
-               dim3((unsigned)((max_new + kPerBlock - 1) / kPerBlock), (unsigned)B), kSlotThreads,
-               0, s);
+    e = launch_after(kv_plan_slots_kernel, p,
+                     dim3((unsigned)((max_new + kPerBlock - 1) / kPerBlock), (unsigned)B),
+                     kSlotThreads, s);
   }
   return cuda_status(e);
 }
@@ -303,14 +335,25 @@ sv_status sv_kv_append(const sv_kv_cache* cache, const void* k, const void* v, i
   p.page = cache->page_size;
   p.num_pages = cache->num_pages;
   p.status = device_status;
+  if ((long long)B * n > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
   const long long row = (long long)cache->head_dim * es;
   const int w = common_width({addr(k), addr(v), addr(cache->k), addr(cache->v), p.in_b, p.in_t,
                               p.c_page, p.c_token, p.c_head, row});
   p.head_chunks = (int)(row / w);
+  if (p.heads > 1 && p.c_head == row) {  // a token's heads are one row
+    p.head_chunks *= p.heads;
+    p.heads = 1;
+  }
+  p.div_n = make_fastdiv(n);
+  p.div_page = make_fastdiv(cache->page_size);
+  p.div_chunks = make_fastdiv(p.head_chunks);
   int sms = 0;
   if (sm_count(&sms) != cudaSuccess) return SV_ERR_CUDA;
-  const long long warps = (long long)B * n;
-  const unsigned grid = (unsigned)std::min<long long>((warps + 7) / 8, (long long)sms * 8);
+  // as many warps as are on the device at once, each with a run of tokens
+  const long long tokens = (long long)B * n, most = (long long)sms * 64;
+  p.per_warp = (int)((tokens + most - 1) / most);
+  const long long warps = (tokens + p.per_warp - 1) / p.per_warp;
+  const unsigned grid = (unsigned)((warps + 7) / 8);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (w) {
     case 16: return cuda_status(launch(kv_append_kernel<uint4>, p, dim3(grid), 256, 0, s));
@@ -449,9 +492,16 @@ sv_status sv_kv_commit(const sv_kv_cache* cache, int layers, int64_t layer_strid
   const int w = common_width(
       {addr(cache->k), addr(cache->v), p.c_layer, p.c_page, p.c_token, p.c_head, row});
   p.head_chunks = (int)(row / w);
-  const long long items = 2LL * layers * cache->heads * p.head_chunks;
+  if (p.heads > 1 && p.c_head == row) {  // a token's heads are one row
+    p.head_chunks *= p.heads;
+    p.heads = 1;
+  }
+  const long long items = 2LL * layers * p.heads * p.head_chunks;
+  if (items > 0x3fffffffLL || cache->page_size > (1 << 30)) return SV_ERR_UNSUPPORTED;
+  p.div_page = make_fastdiv(cache->page_size);
+  p.div_chunks = make_fastdiv(p.heads * p.head_chunks);
+  p.div_head = make_fastdiv(p.head_chunks);
   const long long blocks = (items + kCommitThreads - 1) / kCommitThreads;
-  if (blocks > 0x7fffffffLL) return SV_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)blocks, (unsigned)B);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (w) {
