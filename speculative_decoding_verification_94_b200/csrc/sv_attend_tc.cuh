@@ -390,7 +390,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         qx[j] = on ? __ldg(src + tid % kPieces16) : make_uint4(0, 0, 0, 0);
       }
     };
-    if (cur.v < s.u1) load_q(cur);
+    // ahead of its segment where that takes few registers
+    constexpr bool kQAhead = RT < 128;
+    if (kQAhead && cur.v < s.u1) load_q(cur);
     while (cur.v < s.u1) {
       const int h = cur.seg / cur.mt, row0 = (cur.seg % cur.mt) * RT;
       const int rows = min(RT, cur.q * p.g - row0);
@@ -399,7 +401,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int kv = cur.kv, len = cur.kv + cur.q;
       const int32_t* par = p.parents ? p.parents + (long long)cur.b * p.n : nullptr;
       const int32_t* trow = p.table + (long long)cur.b * p.max_pages;
-      // the rows of q: loaded while the last segment ended
+      // the rows of q
+      if (!kQAhead) load_q(cur);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int c = tid % kPieces16, r = (tid + j * kTcSoftmax) / kPieces16;
@@ -432,24 +435,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // weights: tensor memory is near, registers are not plenty.
         const uint32_t mine = s_at + copy * kKeys;
         const bool tail = (tile0 + k + 1) * kTcU > kv;
-        uint32_t seen[kKeys / 32];
-        if (tail) {
-#pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c)
-            seen[c] = pos0 + c * 32 + 32 > kv
-                          ? att_tail_bits<32>(par, qi, pos0 + c * 32, kv, tree_ok)
-                          : 0xffffffffu;
-        }
+        auto seen = [&](int c) {  // which of chunk c's keys this row sees
+          return pos0 + c * 32 + 32 > kv
+                     ? att_tail_bits<32>(par, qi, pos0 + c * 32, kv, tree_ok)
+                     : 0xffffffffu;
+        };
         float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < kKeys / 32; ++c) {
           uint32_t x[32];
           tc_ld(mine + c * 32, x);
           tc_wait_ld();
           if (tail) {
+            const uint32_t bits = seen(c);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (!(seen[c] >> e & 1u)) x[e] = 0xff800000u;
+              if (!(bits >> e & 1u)) x[e] = 0xff800000u;
           }
           float t2[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -485,15 +486,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const unsigned long long cc = f2_pack(p.scale_log2, p.scale_log2), mm = f2_pack(-ms, -ms);
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
         // P over S: bf16 pairs in the first half of their keys' columns
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < kKeys / 32; ++c) {
           uint32_t x[32];
           tc_ld(mine + c * 32, x);
           tc_wait_ld();
           if (tail) {
+            const uint32_t bits = seen(c);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (!(seen[c] >> e & 1u)) x[e] = 0xff800000u;
+              if (!(bits >> e & 1u)) x[e] = 0xff800000u;
           }
           uint32_t y[16];
 #pragma unroll
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // where the next segment is, and its rows of q
       AttCursor<kTcU, RT, kTcOv> next = cur;
       next.step(p, cnt);
-      if (next.v < s.u1) load_q(next);
+      if (kQAhead && next.v < s.u1) load_q(next);
       if (used && !dead) {
         dead = !__all_sync(0xffffffffu, mbar_wait_bounded(pv_done + w, (tiles_done - 1) & 1));
         if (dead) *s_abort = 1;
@@ -663,7 +665,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           const int col = c0 + j * 4;
           if (fix) {
-            float* av = &a.x;
             const int i = fast_div(row0 + r, p.div_g);
             for (int t = max(0, tile0 * kTcU - kv); t < cur.q; ++t) {
               const int pos = kv + t;
@@ -679,10 +680,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + id * p.c_page +
                                        (long long)(pos - pi * p.page) * p.c_token + h * p.c_head +
                                        col;
-              for (int e = 0; e < 4; ++e) {
-                const float y = __bfloat162float(v[e]);
-                if (not_finite(y)) av[e] += y;
-              }
+              const float y0 = __bfloat162float(v[0]), y1 = __bfloat162float(v[1]);
+              const float y2 = __bfloat162float(v[2]), y3 = __bfloat162float(v[3]);
+              if (not_finite(y0)) a.x += y0;
+              if (not_finite(y1)) a.y += y1;
+              if (not_finite(y2)) a.z += y2;
+              if (not_finite(y3)) a.w += y3;
             }
           }
           if (whole) {
