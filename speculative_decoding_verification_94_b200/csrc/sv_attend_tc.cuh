@@ -34,7 +34,8 @@
 namespace sv {
 
 constexpr int kTcU = 128;            // keys of a tile
-constexpr int kTcOv = 3;             // a segment's beginning and end, in tiles: about 5 us
+// A segment's beginning and end, in tiles: about 5 us with 32 rows, 10 us with 128.
+__host__ __device__ constexpr int tc_ov(int rt) { return rt == 128 ? 7 : rt == 64 ? 4 : 3; }
 constexpr int kTcSoftmax = 256;      // threads of the two warp groups
 constexpr int kTcThreads = 384;      // + two copy warps, product warp, one for the rest
 constexpr int kTcStages = 3;
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_before();
   }
   pdl_launch_dependents();
-  AttCursor<kTcU, RT, kTcOv> cur;
+  AttCursor<kTcU, RT, tc_ov(RT)> cur;
   const AttShare s = att_share<kTcThreads>(p, cur, smem + C::kOffShare);
   __syncthreads();
   tc_fence_after();
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // its copies
     constexpr int kPieces16 = D / 8, kPer = RT * kPieces16 / kTcSoftmax;
     uint4 qx[kPer];
-    auto load_q = [&](const AttCursor<kTcU, RT, kTcOv>& c) {
+    auto load_q = [&](const AttCursor<kTcU, RT, tc_ov(RT)>& c) {
       const int h = c.seg / c.mt, first = (c.seg - h * c.mt) * RT;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
@@ -420,6 +421,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc_fence_before();
       mbar_arrive(q_full);
       if (tile_g == 0) mbar_arrive(q_first);
+      // where the next segment is; its rows of q are brought to L2
+      AttCursor<kTcU, RT, tc_ov(RT)> next = cur;
+      next.step(p, cnt);
+      if (!kQAhead && next.v < s.u1) {
+        const int h2 = next.seg / next.mt;
+        const int qr = (next.seg - h2 * next.mt) * RT + (tid & (RT - 1));
+        if (qr < next.q * p.g && tid / RT * 64 < D) {
+          const int i = fast_div(qr, p.div_g), gi = qr - i * p.g;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(
+              static_cast<const __nv_bfloat16*>(p.q) + next.b * p.q_b + i * p.q_t +
+              (long long)(h2 * p.g + gi) * D + tid / RT * 64));
+        }
+      }
       const int qi = min(fast_div(row0 + row, p.div_g), cur.q - 1);
       float m = -INFINITY, l = 0.f;
       bool tree_ok = true;
@@ -561,9 +575,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ++tiles_done;
       }
       const bool used = w < cnt;
-      // where the next segment is, and its rows of q
-      AttCursor<kTcU, RT, kTcOv> next = cur;
-      next.step(p, cnt);
       if (kQAhead && next.v < s.u1) load_q(next);
       if (used && !dead) {
         dead = !__all_sync(0xffffffffu, mbar_wait_bounded(pv_done + w, (tiles_done - 1) & 1));
