@@ -476,7 +476,8 @@ SV_API sv_status sv_kv_append(const sv_kv_cache* cache, const void* k, const voi
  * Arguments
  *   q [B, n, q_heads, head_dim] of the cache's type, the heads of a token
  *   dense, strides in elements as in sv_kv_append.  out [B, n, q_heads,
- *   head_dim] dense, of the cache's type; lse [B, n, q_heads] fp32 or NULL.
+ *   head_dim] dense, of the cache's type, not over q; lse [B, n, q_heads] fp32
+ *   or NULL.
  *   block_table [B, max_pages], kv_len [B]; q_len [B] or NULL (n everywhere);
  *   parents [B, n] or NULL: int32.
  *   1 <= n <= 1024, q_heads a multiple of heads, scale finite.

@@ -99,16 +99,28 @@ struct AttCursor {
     tile = r < 0 ? 0 : r;
     v = unit + (tile - r);
   }
-  __device__ __forceinline__ void step(const AttendParams& p, int count) {  // within the segment
+  // `count` tiles on, within the segment or to the next one.  All lanes of a
+  // warp come here together: past a request's last segment they look at 32
+  // requests at a time, since a batch may be idle but for a few.
+  __device__ __forceinline__ void step(const AttendParams& p, int count) {
     tile += count;
     v += count;
     if (tile < tiles) return;
     v += OV;
     tile = 0;
-    if (++seg == mt * p.hkv) {
-      seg = 0;
-      do ++b;
-      while (b < p.B && load(p) == 0);
+    if (++seg < mt * p.hkv) return;
+    seg = 0;
+    while (b < p.B) {
+      const int at = b + 1 + (threadIdx.x & 31);
+      int kv1, q1;
+      const bool has = at < p.B && att_lens(p, at, kv1, q1) && q1 > 0;
+      const uint32_t found = __ballot_sync(0xffffffffu, has);
+      if (found) {
+        b += __ffs(found);
+        load(p);
+        return;
+      }
+      b += 32;
     }
   }
 };

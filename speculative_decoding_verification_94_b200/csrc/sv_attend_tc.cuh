@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == 9) {
     // ------------------------------ products ------------------------------
-    if (lane == 0) {
+    {
       constexpr uint32_t kIdQk = tc_idesc(kTcU, false), kIdPv = tc_idesc(D, true);
       const uint32_t qa = smem_u32(s_q);
       int kg = 0, vg = 0;      // tiles whose keys, values have been used
@@ -296,67 +296,69 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       while (cur.v < s.u1 && ok) {
         const int left = cur.tiles - cur.tile;
         const int cnt = s.u1 - cur.v < left ? (int)(s.u1 - cur.v) : left;
-        ok = mbar_wait_bounded(q_full, segs & 1);
-        ++segs;
-        if (!ok) break;
-        tc_fence_after();
-        // whichever product has its operands: S of tile nq (its warp group's
-        // last P is used up), or P V of tile np
-        int nq = 0, np = 0;
-        uint64_t t0 = 0;  // the clock is far away: read once in many idle rounds
-        uint32_t spins = 0;
-        while (np < cnt) {
-          bool idle = true;
-          if (np < nq) {
-            const int w = np & 1, slot = vg % kTcStages;
-            if (mbar_test(p_ready + w, streams[w] & 1) &&
-                mbar_test(v_full + slot, (vg / kTcStages) & 1)) {
-              tc_fence_after();
-              const uint32_t va = smem_u32(smem + C::kOffV + slot * C::kTile);
-              const uint32_t pa = tmem + w * 128, o = tmem + 256 + w * 128;
+        if (lane == 0) {  // one thread issues
+          ok = mbar_wait_bounded(q_full, segs & 1);
+          tc_fence_after();
+          // whichever product has its operands: S of tile nq (its warp group's
+          // last P is used up), or P V of tile np
+          int nq = 0, np = 0;
+          uint64_t t0 = 0;  // the clock is far away: read once in many idle rounds
+          uint32_t spins = 0;
+          while (ok && np < cnt) {
+            bool idle = true;
+            if (np < nq) {
+              const int w = np & 1, slot = vg % kTcStages;
+              if (mbar_test(p_ready + w, streams[w] & 1) &&
+                  mbar_test(v_full + slot, (vg / kTcStages) & 1)) {
+                tc_fence_after();
+                const uint32_t va = smem_u32(smem + C::kOffV + slot * C::kTile);
+                const uint32_t pa = tmem + w * 128, o = tmem + 256 + w * 128;
 #pragma unroll
-              for (int ks = 0; ks < kTcU / 16; ++ks)
-                tc_mma_ts(o, pa + (ks / 2) * 32 + (ks & 1) * 8, tc_desc(va + ks * 2048, C::kHalf),
-                          kIdPv, np >= 2 || ks);
-              tc_commit(pv_done + w);
-              tc_commit(v_empty + slot);
-              ++streams[w];
-              ++vg;
-              ++np;
-              idle = false;
-            }
-          }
-          if (nq < cnt && nq < np + 2) {
-            const int w = nq & 1, slot = kg % kTcStages;
-            if (mbar_test(k_full + slot, (kg / kTcStages) & 1)) {
-              tc_fence_after();
-              const uint32_t ka = smem_u32(smem + C::kOffK + slot * C::kTile);
-#pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t o = (ks / 4) * C::kHalf + (ks % 4) * 32;
-                tc_mma_ss(tmem + w * 128, tc_desc(qa + o, 16), tc_desc(ka + o, 16), kIdQk, ks > 0);
+                for (int ks = 0; ks < kTcU / 16; ++ks)
+                  tc_mma_ts(o, pa + (ks / 2) * 32 + (ks & 1) * 8, tc_desc(va + ks * 2048, C::kHalf),
+                            kIdPv, np >= 2 || ks);
+                tc_commit(pv_done + w);
+                tc_commit(v_empty + slot);
+                ++streams[w];
+                ++vg;
+                ++np;
+                idle = false;
               }
-              tc_commit(s_full + w);
-              tc_commit(k_empty + slot);
-              ++kg;
-              ++nq;
-              idle = false;
             }
-          }
-          if (!idle) {
-            spins = 0;
-          } else if ((++spins & 1023) == 0) {
-            const uint64_t now = globaltimer_ns();
-            if (spins == 1024) t0 = now;
-            if (now - t0 > kWaitLimitNs) {
-              ok = false;
-              break;
+            if (nq < cnt && nq < np + 2) {
+              const int w = nq & 1, slot = kg % kTcStages;
+              if (mbar_test(k_full + slot, (kg / kTcStages) & 1)) {
+                tc_fence_after();
+                const uint32_t ka = smem_u32(smem + C::kOffK + slot * C::kTile);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                  const uint32_t o = (ks / 4) * C::kHalf + (ks % 4) * 32;
+                  tc_mma_ss(tmem + w * 128, tc_desc(qa + o, 16), tc_desc(ka + o, 16), kIdQk, ks > 0);
+                }
+                tc_commit(s_full + w);
+                tc_commit(k_empty + slot);
+                ++kg;
+                ++nq;
+                idle = false;
+              }
+            }
+            if (!idle) {
+              spins = 0;
+            } else if ((++spins & 1023) == 0) {
+              const uint64_t now = globaltimer_ns();
+              if (spins == 1024) t0 = now;
+              if (now - t0 > kWaitLimitNs) {
+                ok = false;
+                break;
+              }
             }
           }
         }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ++segs;
         cur.step(p, cnt);
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         *s_abort = 1;
         kv_flag(p.status, SV_DEV_TIMEOUT);
       }

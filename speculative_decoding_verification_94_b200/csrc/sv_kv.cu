@@ -387,7 +387,7 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_st
     return SV_ERR_INVALID_ARG;
   if (B == 0) return SV_OK;
   const int es = esize(cache->dtype);
-  if (!q || !out || !block_table || !kv_len || !aligned(q, es) || !aligned(out, es) ||
+  if (!q || !out || out == q || !block_table || !kv_len || !aligned(q, es) || !aligned(out, es) ||
       !aligned(block_table, 4) || !aligned(kv_len, 4) || !aligned_or_null(q_len, 4) ||
       !aligned_or_null(parents, 4) || !aligned_or_null(lse, 4) ||
       !aligned_or_null(device_status, 4))

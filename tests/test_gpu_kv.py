@@ -270,6 +270,10 @@ CASES = [
     (1, 12, 8, 1, 64, 16, [5003]),
     (200, 1, 2, 1, 64, 16, [0, 1, 40, 90]),  # more requests than threads of a warp
     (700, 1, 1, 1, 64, 16, [3, 0, 17]),      # more requests than threads of a block
+    (2, 20, 16, 2, 128, 24, [100, 259]),    # 160 rows, pages that no tile is a multiple of
+    (2, 20, 16, 2, 64, 4, [100, 259]),      # and pages too small for a tile's boxes
+    (2, 9, 8, 2, 128, 8, [100, 259]),       # 36 rows, the smallest pages that boxes take
+    (2, 20, 16, 2, 128, 256, [100, 700]),   # pages larger than a tile
 ]
 
 
@@ -383,6 +387,73 @@ def test_attend_bad_inputs_fail_only_their_rows(n, hq, d):
         out, lse, st = call_attend(t)
         assert st == sv.SV_DEV_BAD_TREE and torch.isnan(out[3, n - 1]).all()
         assert torch.isfinite(out[:3].float()).all()
+
+
+@pytest.mark.parametrize("n,hq,dtype", [(1, 4, "bf16"), (3, 14, "bf16"), (10, 16, "bf16"),
+                                        (40, 8, "bf16"), (2, 8, "f32")])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30, 4.0])
+def test_attend_scales(n, hq, dtype, scale):
+    s = scenario(2, n, hq, 2, 64, 16, [33, 200], dtype, tree=True, seed=13, q_scale=0.5)
+    s["scale"] = scale
+    out, lse, st = call_attend(s)
+    assert st == 0
+    check_attend(s, out, lse)
+
+
+@pytest.mark.parametrize("n,g", [(1, 3), (3, 7), (9, 4), (20, 8)])
+@pytest.mark.parametrize("shift", [1, 2, 4])
+def test_attend_queries_off_16_bytes(n, g, shift):
+    s = scenario(2, n, 2 * g, 2, 128, 16, [20, 300], "bf16", seed=17)
+    buf = torch.empty(s["q"].numel() + shift, dtype=torch.bfloat16, device=DEV)
+    q = buf[shift:].view(s["q"].shape)
+    q.copy_(s["q"])
+    s["q"] = q
+    out, lse, st = call_attend(s)
+    assert st == 0
+    check_attend(s, out, lse)
+
+
+@pytest.mark.parametrize("n,hq,dtype", [(1, 4, "bf16"), (3, 14, "bf16"), (20, 16, "bf16"),
+                                        (4, 8, "f32")])
+def test_attend_a_batch_that_is_idle_but_for_a_few(n, hq, dtype):
+    s = scenario(300, n, hq, 2, 64, 16, [5, 90, 40], dtype, seed=19)
+    s["q_len"] = [n if b in (0, 7, 150, 298) else 0 for b in range(300)]
+    s["kv_len"] = [x if m else -5 for x, m in zip(s["kv_len"], s["q_len"])]  # not looked at
+    out, lse, st = call_attend(s)
+    assert st == 0
+    check_attend(s, out, lse)
+
+
+@pytest.mark.parametrize("n,hq", [(1, 4), (20, 4)])
+def test_attend_finds_one_bad_page_among_many(n, hq):
+    """More pages than a block looks at in one go."""
+    num = 90000
+    g = torch.Generator(device=DEV).manual_seed(0)
+    k = torch.randn(num, 8, 1, 64, generator=g, device=DEV).bfloat16()
+    v = torch.randn(num, 8, 1, 64, generator=g, device=DEV).bfloat16()
+    q = torch.randn(1, n, hq, 64, generator=g, device=DEV).bfloat16()
+    table = torch.randperm(num, generator=g, device=DEV).int()[None].contiguous()
+    kv_len = i32([num * 8 - n])
+    st = status()
+    o = sv.sv_kv_attend(q, k, v, table, kv_len, device_status=st)
+    assert int(st.item()) == 0 and torch.isfinite(o["out"].float()).all()
+    # against plain attention in float64 over the gathered cache
+    kk, vv = (x[table[0].long()].view(-1, 64).double() for x in (k, v))
+    z = (q[0].double().view(-1, 64) @ kk.T) * 0.125
+    keep = torch.arange(num * 8, device=DEV)[None, :] <= num * 8 - n + torch.arange(
+        n, device=DEV).repeat_interleave(hq)[:, None]
+    w = torch.softmax(torch.where(keep, z, float("-inf")), -1)
+    ref, absv = w @ vv, w @ vv.abs()
+    # 7e5 terms of the sums and a maximum that may grow in each of their tiles,
+    # and half a step of bf16 for the weights and for the result
+    tol = absv * (2 * 7.2e5 * 1.4 * 2.0 ** -24 + 2.0 ** -8) + 2.0 ** -8 * ref.abs()
+    assert ((o["out"][0].double().view(-1, 64) - ref).abs() <= tol).all()
+    for at in (5, 44321, num - 1):
+        bad = table.clone()
+        bad[0, at] = num
+        st.zero_()
+        o = sv.sv_kv_attend(q, k, v, bad, kv_len, device_status=st)
+        assert int(st.item()) == sv.SV_DEV_BAD_INDEX and torch.isnan(o["out"]).all()
 
 
 def test_attend_offsets_past_32_bits():
@@ -556,9 +627,10 @@ def test_binding_refuses_mismatched_tensors():
     with pytest.raises(sv.SVError) as e:
         attend(q=s["q"][:, :, :3].contiguous())  # 3 query heads over 2 key heads
     assert e.value.status == sv.SV_ERR_INVALID_ARG
-    with pytest.raises(sv.SVError) as e:
-        attend(scale=float("inf"))
-    assert e.value.status == sv.SV_ERR_INVALID_ARG
+    for kw in (dict(scale=float("inf")), dict(out=dict(out=s["q"]))):  # out over q
+        with pytest.raises(sv.SVError) as e:
+            attend(**kw)
+        assert e.value.status == sv.SV_ERR_INVALID_ARG
 
 
 # ---------------------------------------------------------------------------

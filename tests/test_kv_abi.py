@@ -86,7 +86,7 @@ def test_attend_validates(lib):
 
     def call(c=None, **kw):
         a = dict(q=F, bs=1024, ts=256, B=4, n=4, hq=4, table=F, max_pages=8, kv_len=F, q_len=F,
-                 parents=F, scale=0.125, out=F, lse=F, ws=F, wsb=big, status=None, stream=None)
+                 parents=F, scale=0.125, out=F + 4096, lse=F, ws=F, wsb=big, status=None, stream=None)
         a.update(kw)
         return lib.sv_kv_attend(ctypes.byref(c or cache()), *a.values())
     for kw in BAD_CACHES:
@@ -96,7 +96,7 @@ def test_attend_validates(lib):
                dict(parents=F + 2), dict(lse=F + 2), dict(status=F + 2), dict(B=-1), dict(n=0),
                dict(n=1025), dict(hq=0), dict(hq=3), dict(max_pages=0),
                dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38),
-               dict(bs=-1), dict(ts=-1)):
+               dict(bs=-1), dict(ts=-1), dict(out=F)):
         assert call(**kw) == E, kw
     assert call(hq=1 << 17) == U
     need = lib.sv_kv_attend_scratch_size(4, 4, 4, 2, 64, sv.SV_BF16)
