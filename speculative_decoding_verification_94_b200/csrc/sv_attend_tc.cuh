@@ -546,28 +546,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             *s_abort = 1;
             break;
           }
-          const int pos = (tile0 + k) * kTcU + lr;
-          if (pos >= kv && (pos >= len || cur.q > 1)) {
-            unsigned char* vrow = smem + C::kOffV + slot * C::kTile + lr * 128;
-#pragma unroll 1
-            for (int c = 0; c < D / 8; ++c) {
-              uint4* at = reinterpret_cast<uint4*>(vrow + (c / 8) * C::kHalf + (c % 8) * 16);
-              uint32_t y[4] = {0, 0, 0, 0};
-              if (pos < len) {
-                const uint4 v = *at;
-                y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
-                bool any = false;
+          // Pages past the end were copied as zeros already.
+          const int pos0v = (tile0 + k) * kTcU;
+          const int end = (fast_div(len - 1, p.div_page) + 1) * p.page - pos0v;
+          constexpr int kChunks = D / 8, kRowsPer = 32 / kChunks;
+          for (int r = max((cur.q > 1 ? kv : len) - pos0v, 0) + quad * kRowsPer + lane / kChunks;
+               r < min(end, kTcU); r += 4 * kRowsPer) {
+            const int c = lane % kChunks;
+            uint4* at = reinterpret_cast<uint4*>(smem + C::kOffV + slot * C::kTile +
+                                                 (c / 8) * C::kHalf + r * 128 + (c % 8) * 16);
+            uint32_t y[4] = {0, 0, 0, 0};
+            if (pos0v + r < len) {
+              const uint4 v = *at;
+              y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+              bool any = false;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  any |= bf16x2_not_finite(y[e]);
-                  if ((y[e] & 0x7f80u) == 0x7f80u) y[e] &= 0xffff0000u;
-                  if ((y[e] & 0x7f800000u) == 0x7f800000u) y[e] &= 0xffffu;
-                }
-                if (!any) continue;
-                *s_fix = 1;
+              for (int e = 0; e < 4; ++e) {
+                any |= bf16x2_not_finite(y[e]);
+                if ((y[e] & 0x7f80u) == 0x7f80u) y[e] &= 0xffff0000u;
+                if ((y[e] & 0x7f800000u) == 0x7f800000u) y[e] &= 0xffffu;
               }
-              *at = make_uint4(y[0], y[1], y[2], y[3]);
+              if (!any) continue;
+              *s_fix = 1;
             }
+            *at = make_uint4(y[0], y[1], y[2], y[3]);
           }
           fence_async_smem();
         }
