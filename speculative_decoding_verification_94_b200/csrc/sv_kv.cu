@@ -9,6 +9,7 @@
 #include "sv_attend_f32.cuh"
 #include "sv_attend_mma.cuh"
 #include "sv_attend_tc.cuh"
+#include "sv_attend_tf32.cuh"
 #include "sv_kv_pages.cuh"
 
 namespace sv {
@@ -226,8 +227,7 @@ cudaError_t launch_f32(AttendParams& p, cudaStream_t s) {
   if (rows <= 8)
     return launch_attend<float, D, 8>(attend_f32_kernel<D, 8>, p, kF32Threads, F32Cfg<D, 8>::kSmem,
                                       s);
-  return launch_attend<float, D, 16>(attend_f32_kernel<D, 16>, p, kF32Threads,
-                                     F32Cfg<D, 16>::kSmem, s);
+  return launch_attend<float, D, 16>(attend_tf32_kernel<D>, p, kF32Threads, Tf32Cfg<D>::kSmem, s);
 }
 
 }  // namespace

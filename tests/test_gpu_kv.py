@@ -225,8 +225,11 @@ def check_attend(s, out, lse, rows=None):
     maximum can grow; sums of N terms add N eps.  Numerator and denominator
     both have these errors (factor 2).  bf16 weights enter the numerator only:
     as a sum of two bf16 they are off by 2^-16 up to 16 rows a key head, as
-    one bf16 by half a step, 2^-8, beyond (sum |dp v| <= 2^-8 sum p |v|).  The
-    output then rounds by half a step of its type."""
+    one bf16 by half a step, 2^-8, beyond (sum |dp v| <= 2^-8 sum p |v|).  fp32
+    products of more than 8 rows go through two-part tf32 and are off by 20 eps
+    each: 20 eps size of a score, within 2 (d + 4) eps size where d >= 64, and
+    20 eps of the numerator, counted for both types.  The output then rounds
+    by half a step of its type."""
     ref, rl, size, absv = O.attend(host(s["q"]), host(s["kc"]), host(s["vc"]), s["table"],
                                    s["kv_len"], s["q_len"], s["parents"], s["scale"])
     d = s["q"].shape[-1]
@@ -235,7 +238,7 @@ def check_attend(s, out, lse, rows=None):
     n_keys = np.array(s["kv_len"])[:, None, None] + s["q"].shape[1]
     w = (2 * (d + 4) * size + n_keys + 6 * (n_keys / 16 + 2)) * eps
     rows = s["q"].shape[1] * s["q"].shape[2] // s["kc"].shape[2]
-    rel = 2 * w + (0.0 if not bf else 2.0 ** -16 if rows <= 16 else 2.0 ** -8)
+    rel = 2 * w + 20 * eps + (0.0 if not bf else 2.0 ** -16 if rows <= 16 else 2.0 ** -8)
     tol = rel[..., None] * absv + (2.0 ** -8 if bf else 2.0 ** -24) * np.abs(ref) + 1e-37
     got, gl = host(out), lse.cpu().numpy().astype(np.float64)
     for b in range(got.shape[0]):
