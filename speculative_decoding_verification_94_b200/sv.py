@@ -10,6 +10,7 @@ operation each call performs and the pages it restates.
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 from pathlib import Path
 
@@ -600,19 +601,25 @@ def _rows(t, name: str, dev, B: int) -> tuple[int, int]:
     raise ValueError(f"{name} must be a matrix of {B} rows")
 
 
-def _kv_cache(k: torch.Tensor, v: torch.Tensor) -> sv_kv_cache:
+def _kv_cache(k: torch.Tensor, v: torch.Tensor, layered: bool = False):
     """Descriptor of caches [num_pages, page_size, heads, head_dim]: any
-    strides (the same for both) with a dense last dimension."""
-    for t, name in ((k, "k_cache"), (v, "v_cache")):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
+    strides (the same for both) with a dense last dimension.  With `layered`
+    they may be [layers, ...]: (descriptor, layers, layer stride)."""
+    if not (isinstance(k, torch.Tensor) and k.is_cuda):
+        raise TypeError("k_cache must be a CUDA tensor")
+    if not (isinstance(v, torch.Tensor) and v.is_cuda):
+        raise TypeError("v_cache must be a CUDA tensor")
     shape, st = k.shape, k.stride()
-    if len(shape) != 4 or shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+    if shape != v.shape or k.dtype != v.dtype or k.device != v.device or \
+            not (len(shape) == 4 or layered and len(shape) == 5):
         raise ValueError("k_cache and v_cache must be [num_pages, page_size, heads, head_dim] of "
                          "one shape, type and device")
-    if st != v.stride() or (st[3] != 1 and shape[3] > 1):
+    if st != v.stride() or (st[-1] != 1 and shape[-1] > 1):
         raise ValueError("k_cache and v_cache must have the same strides and dense rows")
-    return sv_kv_cache(k.data_ptr(), v.data_ptr(), _dtype_code(k), *shape, *st[:3])
+    c = sv_kv_cache(k.data_ptr(), v.data_ptr(), _dtype_code(k), *shape[-4:], *st[-4:-1])
+    if not layered:
+        return c
+    return (c, shape[0], st[0]) if len(shape) == 5 else (c, 1, 0)
 
 
 def _token_rows(t: torch.Tensor, name: str, cache: torch.Tensor, heads: int | None):
@@ -688,10 +695,16 @@ def sv_kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cac
             _ptr(device_status, "device_status", torch.int32, dev, 1))
 
 
+@functools.lru_cache(maxsize=None)  # of the sizes alone
+def _attend_scratch_size(n: int, q_heads: int, heads: int, head_dim: int, code: int) -> int:
+    return int(lib().sv_kv_attend_scratch_size(1, n, q_heads, heads, head_dim, code))
+
+
 def sv_kv_attend_scratch_size(B: int, n: int, q_heads: int, heads: int, head_dim: int,
-                                dtype: torch.dtype) -> int:
+                              dtype: torch.dtype) -> int:
+    """Bytes of scratch that sv_kv_attend needs (the same for every B)."""
     code = SV_BF16 if dtype == torch.bfloat16 else SV_F32
-    return int(lib().sv_kv_attend_scratch_size(B, n, q_heads, heads, head_dim, code))
+    return _attend_scratch_size(n, q_heads, heads, head_dim, code)
 
 
 def sv_kv_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -713,12 +726,10 @@ def sv_kv_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         o["out"] = _empty((B, n, hq, d), q.dtype, dev, stream)
     if "lse" not in o:
         o["lse"] = _empty((B, n, hq), torch.float32, dev, stream)
-    L = lib()
     if scratch is None:
-        scratch = _empty(L.sv_kv_attend_scratch_size(B, n, hq, c.heads, d, c.dtype), torch.uint8,
-                         dev, stream)
+        scratch = _empty(_attend_scratch_size(n, hq, c.heads, d, c.dtype), torch.uint8, dev, stream)
     table, max_pages = _rows(block_table, "block_table", dev, B)
-    _launch(L.sv_kv_attend, "sv_kv_attend", dev, stream, ctypes.byref(c), q.data_ptr(), sb, st, B,
+    _launch(lib().sv_kv_attend, "sv_kv_attend", dev, stream, ctypes.byref(c), q.data_ptr(), sb, st, B,
             n, hq, table, max_pages, _ptr(kv_len, "kv_len", i32, dev, B),
             _ptr(q_len, "q_len", i32, dev, B), _ptr(parents, "parents", i32, dev, B * n),
             d ** -0.5 if scale is None else scale, _ptr(o["out"], "out", q.dtype, dev, B * n * hq * d),
@@ -735,18 +746,10 @@ def sv_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torc
     Caches [num_pages, page_size, heads, head_dim] of one layer, or [layers,
     ...] of all of them; accepted_nodes [B, max_depth + 1] and accepted_len
     [B] as sv_verify_tree_* return them."""
-    layers, layer_stride = 1, 0
-    k0, v0 = k_cache, v_cache
-    if isinstance(k_cache, torch.Tensor) and isinstance(v_cache, torch.Tensor) and \
-            k_cache.dim() == 5 and v_cache.dim() == 5:
-        layers, layer_stride = k_cache.shape[0], k_cache.stride(0)
-        if v_cache.shape[0] != layers or (layers > 1 and v_cache.stride(0) != layer_stride):
-            raise ValueError("k_cache and v_cache must have the same layers")
-        if layers == 0:
-            return
-        k0, v0 = k_cache[0], v_cache[0]
-    c = _kv_cache(k0, v0)
-    dev, i32 = k0.device, torch.int32
+    c, layers, layer_stride = _kv_cache(k_cache, v_cache, True)
+    if layers == 0:
+        return
+    dev, i32 = k_cache.device, torch.int32
     _dev(kv_len, "kv_len", i32)
     B = kv_len.numel()
     table, max_pages = _rows(block_table, "block_table", dev, B)
