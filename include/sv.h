@@ -532,15 +532,18 @@ SV_API sv_status sv_kv_commit(const sv_kv_cache* cache, int layers, int64_t laye
  *   SV_KNOB_STREAM_COUNT  two-kernel streaming pass: 1 static partition,
  *                         2 dynamic items with in-stream row completion
  *   SV_KNOB_STREAM_W      two-kernel streaming chunk, a multiple of 1024 entries
- *   SV_KNOB_WAIT_NS       time limit of every bounded wait of the chain kernel,
- *                         in ns (default 1 s); a wait that runs out sets
- *                         SV_DEV_TIMEOUT
+ *   SV_KNOB_WAIT_NS       time limit of every bounded wait of the chain kernel and
+ *                         of sv_kv_attend, in ns (default 1 s); a wait that runs
+ *                         out sets SV_DEV_TIMEOUT
  *   SV_KNOB_STALL         1: the chain kernel's warp that reduces the first
  *                         slice of request 0's first row waits on a barrier
  *                         nothing arrives on, for a quarter of the wait limit,
  *                         so that the wait runs out (a test of the timeout
  *                         path: request 0 fails with SV_DEV_TIMEOUT, everything
  *                         else completes)
+ *                         sv_kv_attend on the tensor-memory path: the values of
+ *                         the first tile are never copied; the outputs that its
+ *                         block has a part in are NaN
  *   SV_KNOB_STAGES        chain kernel ring stages per CTA, 2..8
  *   SV_KNOB_ORDER         chain kernel tile order: 1 the tiles of a row
  *                         consecutive, 2 the requests innermost

@@ -1,9 +1,8 @@
-// sv_attend_f32.cuh -- fp32 attention of head sizes 64 and 128, up to 16 rows
-// at a time.
+// sv_attend_f32.cuh -- fp32 attention of head sizes 64 and 128, up to 8 rows.
 //
-// fp32 caches keep fp32 products, so there is no tensor core for them: a key
-// costs 4 D rows operations against 8 D bytes, and up to about 8 rows the read
-// of the cache is the bound, beyond it the fp32 pipe.  The frame is that of
+// A key costs 4 D rows operations against 8 D bytes: up to about 8 rows the
+// read of the cache is the bound (32 requests of 4000 keys, 8 key heads, 4
+// rows: 1.06 GB in 200 us, 5.3 TB/s), beyond it the fp32 pipe.  The frame is that of
 // the bf16 kernel of few rows: four warps, each with its own ring of 8-key
 // steps, its own softmax and output.  Scores: four lanes share a key, each
 // takes every fourth 16 bytes of the row; their sums are exchanged so that

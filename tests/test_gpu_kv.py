@@ -538,6 +538,24 @@ def test_attend_captured_and_replayed_with_new_lengths():
                 assert torch.equal(o[k].view(bits), want[k].view(bits))
 
 
+@pytest.mark.parametrize("n,d,lens", [(10, 128, [900, 300, 64]), (40, 64, [20, 2000, 64]),
+                                      (20, 128, [5000])])
+def test_attend_bounded_wait_runs_out_and_reports(n, d, lens):
+    """The test hook leaves out one copy: the waits for it give up after 20 ms,
+    the call returns, the first block's rows are NaN, the last request is
+    whole, and so is the next call."""
+    s = scenario(4, n, 8, 2, d, 16, lens, "bf16", seed=31)
+    clean = call_attend(s)
+    assert clean[2] == 0
+    with sv.knobs(wait_ns=20_000_000, stall=1):
+        out, lse, st = call_attend(s)
+    assert st == sv.SV_DEV_TIMEOUT and sv.sv_device_status_check(st) == sv.SV_ERR_TIMEOUT
+    assert torch.isnan(out[0, 0, 0]).all() and torch.isnan(lse[0, 0, 0])
+    assert torch.equal(out[3], clean[0][3]) and torch.equal(lse[3], clean[1][3])
+    again = call_attend(s)
+    assert again[2] == 0 and torch.equal(again[0], clean[0]) and torch.equal(again[1], clean[1])
+
+
 # ---------------------------------------------------------------------------
 # commit
 # ---------------------------------------------------------------------------
