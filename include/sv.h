@@ -429,7 +429,8 @@ typedef struct sv_kv_cache {
  *   kv_len_out, pages_out, q_len [B], free_count_out [1]: out; each may be
  *   the array of an input.  slot_map [B, max_new] int64, positions
  *   [B, max_new] int32 (or NULL): out.
- *   0 <= B <= 8192, B * max_pages < 2^31, B * max_new < 2^31.
+ *   0 <= B <= 8192, B * max_pages < 2^31, B * max_new < 2^31; page_size and
+ *   max_new up to 2^30.
  *   A request with a length out of range (L_b + new_len[b] beyond max_pages
  *   pages, accepted_len[b] >= written[b] > 0, committed tokens without a page, ...)
  *   is left as it is, gets no new tokens and sets SV_DEV_BAD_LEN.  A page id
@@ -471,7 +472,8 @@ SV_API sv_status sv_kv_append(const sv_kv_cache* cache, const void* k, const voi
  *   out[b, i, x] = sum_j softmax_j(scale * q[b, i, x] . k_j) v_j,
  *   lse[b, i, x] = log sum_j exp(scale * q[b, i, x] . k_j).
  *   A key that a row does not attend to never affects it, whatever the cache
- *   holds there.  Tokens i >= q_len[b] give zeros and lse -inf.
+ *   holds there.  A value that it does attend to and that is not finite makes
+ *   that element of the output not finite; q and the attended keys are finite.  Tokens i >= q_len[b] give zeros and lse -inf.
  *
  * Arguments
  *   q [B, n, q_heads, head_dim] of the cache's type, the heads of a token
@@ -511,7 +513,7 @@ SV_API sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t b
  * The next sv_kv_plan then commits accepted_len[b] + 1 tokens.
  *   accepted_nodes [B, width] and accepted_len [B] as sv_verify_tree_* give
  *   them (width = max_depth + 1 <= 1024; the path ascends from node 0; entries
- *   past the path are not read; accepted_len -1 or 0 moves nothing).
+ *   past the path are ignored; accepted_len -1 or 0 moves nothing).
  *   A path that does not ascend from 0 sets SV_DEV_BAD_TREE, a position
  *   outside the table or accepted_len >= width SV_DEV_BAD_LEN, a bad page
  *   SV_DEV_BAD_INDEX; such a request's cache is left as it is.

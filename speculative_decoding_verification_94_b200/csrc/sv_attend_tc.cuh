@@ -570,10 +570,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           // Pages past the end were copied as zeros already.
           const int pos0v = (tile0 + k) * kTcU;
-          const int end = (fast_div(len - 1, p.div_page) + 1) * p.page - pos0v;
+          const long long page_end = (long long)(fast_div(len - 1, p.div_page) + 1) * p.page - pos0v;
+          const int end = page_end < kTcU ? (int)page_end : kTcU;
           constexpr int kChunks = D / 8, kRowsPer = 32 / kChunks;
           for (int r = max((cur.q > 1 ? kv : len) - pos0v, 0) + quad * kRowsPer + lane / kChunks;
-               r < min(end, kTcU); r += 4 * kRowsPer) {
+               r < end; r += 4 * kRowsPer) {
             const int c = lane % kChunks;
             uint4* at = reinterpret_cast<uint4*>(smem + C::kOffV + slot * C::kTile +
                                                  (c / 8) * C::kHalf + r * 128 + (c % 8) * 16);
@@ -707,10 +708,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const int pos = kv + t;
               if (pos >= (tile0 + cnt) * kTcU) break;
               int up = i;
-              if (par)
-                while (up > t) up = par[up];
-              else
+              if (!par) {
                 up = t <= i ? t : -1;
+              } else {
+                while (up > t) {
+                  const int above = par[up];
+                  up = above < up ? above : -1;  // a bad parent ends the walk
+                }
+              }
               if (up != t) continue;
               const int pi = pos / p.page, id = trow[pi];
               if (id < 0 || id >= p.num_pages) continue;

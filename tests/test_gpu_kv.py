@@ -369,6 +369,33 @@ def test_attend_infinite_values_reach_the_rows_that_see_them(n, hq):
     assert torch.isinf(out[:, 1:, :, 3]).all() and torch.isnan(out[:, 1:, :, 8]).all()
 
 
+@pytest.mark.parametrize("n,hq,dtype", [(6, 4, "bf16"), (20, 16, "bf16"), (40, 8, "bf16"),
+                                        (6, 4, "f32"), (20, 16, "f32")])
+def test_attend_bad_parents_beside_infinite_values(n, hq, dtype):
+    """Walks up a tree end at a bad parent, in the search for values that are
+    not finite too."""
+    s = scenario(3, n, hq, 2, 128, 16, [40, 3, 90], dtype, tree=True, seed=8)
+    t = dict(s, parents=[list(r) for r in s["parents"]], vc=s["vc"].clone())
+    t["parents"][0][n - 1] = n - 1          # itself
+    t["parents"][0][n - 2] = n - 1          # each other
+    t["parents"][1][n - 1] = n + 5          # no node
+    t["parents"][1][n - 2] = -7
+    for b in range(3):
+        at = s["kv_len"][b]
+        t["vc"][s["table"][b][at // 16], at % 16, :, 5] = float("inf")
+    out, lse, st = call_attend(t)
+    assert st == sv.SV_DEV_BAD_TREE
+    for b in range(2):
+        assert torch.isnan(out[b, n - 2:]).all() and torch.isnan(lse[b, n - 2:]).all()
+    # the sound request: infinite where the root is an ancestor
+    clean = call_attend(s)[0]
+    keep = [c for c in range(128) if c != 5]
+    assert torch.equal(out[2][..., keep], clean[2][..., keep])
+    for i in range(n):
+        root = 0 in O.ancestors(s["parents"][2], i)
+        assert bool(torch.isinf(out[2, i, :, 5]).all()) == root
+
+
 @pytest.mark.parametrize("n,hq,d", [(1, 4, 128), (8, 8, 64), (20, 8, 128), (3, 4, 40)])
 def test_attend_bad_inputs_fail_only_their_rows(n, hq, d):
     s = scenario(4, n, hq, 2, d, 16, [40, 40, 40, 40], "bf16", tree=True, seed=3)
