@@ -1,4 +1,5 @@
-"""Build libsv.so (the CUDA library) in-tree for sm_100a with nvcc."""
+"""Build libsv.so (the CUDA library) in-tree for sm_100a with nvcc, and the
+native part of its Python binding with the host compiler."""
 from __future__ import annotations
 
 import os
@@ -10,17 +11,30 @@ PKG = Path(__file__).resolve().parent
 CSRC = PKG / "csrc"
 SOURCES = ["sv_api.cu", "sv_chain_bf16.cu", "sv_chain_f32.cu", "sv_kv.cu"]
 LIB = PKG / "libsv.so"
+BIND = PKG / "_svkv.so"  # Python module over libsv.so, for the paged cache calls
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-fvisibility=hidden"]
 
 
 def _stale() -> bool:
-    if not LIB.exists():
+    if not LIB.exists() or not BIND.exists():
         return True
-    t = LIB.stat().st_mtime
+    t = min(LIB.stat().st_mtime, BIND.stat().st_mtime)
     deps = list(CSRC.glob("*")) + [PKG.parent / "include" / "sv.h", Path(__file__)]
     return any(d.stat().st_mtime > t for d in deps if d.exists())
+
+
+def _bind_command(obj: Path) -> list:
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import CUDA_HOME, include_paths
+    inc = [*include_paths(), sysconfig.get_paths()["include"],
+           os.path.join(CUDA_HOME or "/usr/local/cuda", "include")]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f"-isystem{d}" for d in inc], "-c", str(CSRC / "sv_bind.cpp"), "-o", str(obj)]
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int = 4) -> Path:
@@ -38,6 +52,10 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 4) -> Path:
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    tmp_bind = BIND.with_suffix(f".{os.getpid()}.tmp")
+    procs.append(("sv_bind.cpp", subprocess.Popen(_bind_command(objdir / "sv_bind.o"),
+                                                  stdout=subprocess.PIPE,
+                                                  stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -51,6 +69,12 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 4) -> Path:
     subprocess.run([nvcc, *ARCH, "-shared", "-Xcompiler", "-fPIC", *map(str, objs), "-o", str(tmp)],
                    check=True)
     os.replace(tmp, LIB)
+    from torch.utils.cpp_extension import library_paths
+    libs = [f"-L{d}" for d in library_paths()]
+    subprocess.run([os.environ.get("CXX", "g++"), "-shared", str(objdir / "sv_bind.o"), "-o",
+                    str(tmp_bind), f"-L{PKG}", "-l:libsv.so", "-Wl,-rpath,$ORIGIN", *libs, "-lc10",
+                    "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], check=True)
+    os.replace(tmp_bind, BIND)
     return LIB
 
 

@@ -1,7 +1,7 @@
 """Python binding of libsv (the C ABI declared in include/sv.h).
 
-Argument marshalling only: every step of verification runs in the CUDA
-kernels of libsv.so.  PyTorch provides device memory and the current stream.
+Argument marshalling only (by ctypes; for the paged cache calls by _svkv.so):
+every step of verification runs in the CUDA kernels of libsv.so.  PyTorch provides device memory and the current stream.
 There is no CPU fallback: if libsv.so is missing, every call raises.
 
 Function names and argument order follow the C ABI; see include/sv.h for the
@@ -10,7 +10,6 @@ operation each call performs and the pages it restates.
 from __future__ import annotations
 
 import ctypes
-import functools
 import threading
 from pathlib import Path
 
@@ -554,89 +553,38 @@ def sv_kd_grad(topk_logp: torch.Tensor, topk_idx: torch.Tensor, draft: torch.Ten
 # ---------------------------------------------------------------------------
 # The paged key-value cache of a verification step
 # ---------------------------------------------------------------------------
-def _launch(fn, what: str, dev: torch.device, stream, *args) -> None:
-    """Calls the C function on `stream` (None: the current one of `dev`) with
-    `dev` as the current device."""
-    idx = dev.index
-    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(idx)
-    if torch._C._cuda_getDevice() == idx:
-        rc = fn(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, s)
-    if rc != SV_OK:
-        raise SVError(what, rc)
+_kv = None
 
 
-def _empty(shape, dtype, dev, stream):
-    """Device memory that belongs to the stream of the call."""
+def _native():
+    """The native half of the binding of these calls (raises if it has not
+    been built)."""
+    global _kv
+    if _kv is None:
+        path = _LIB_PATH.parent / "_svkv.so"
+        if not path.exists():
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m speculative_decoding_verification_94_b200.build`")
+        lib()
+        from . import _svkv
+        _kv = _svkv
+    return _kv
+
+
+def _call(what: str, fn, stream, *args):
+    """Runs a call on `stream` (None: the current one); its result, or the
+    error its status stands for."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
-
-
-def _ptr(t, name: str, dtype, dev, numel: int):
-    """Data pointer of a dense device tensor of `numel` entries (None stays
-    None), checked."""
-    if t is None:
-        return None
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and \
-            t.is_contiguous() and t.numel() == numel:
-        return t.data_ptr()
-    _dev(t, name, dtype)
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
-    raise ValueError(f"{name} must have {numel} entries, got {t.numel()}")
-
-
-def _rows(t, name: str, dev, B: int) -> tuple[int, int]:
-    """Data pointer and width of a dense int32 matrix of B rows."""
-    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == dev and \
-            t.is_contiguous() and t.dim() == 2 and t.shape[0] == B:
-        return t.data_ptr(), t.shape[1]
-    _dev(t, name, torch.int32)
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
-    raise ValueError(f"{name} must be a matrix of {B} rows")
-
-
-def _kv_cache(k: torch.Tensor, v: torch.Tensor, layered: bool = False):
-    """Descriptor of caches [num_pages, page_size, heads, head_dim]: any
-    strides (the same for both) with a dense last dimension.  With `layered`
-    they may be [layers, ...]: (descriptor, layers, layer stride)."""
-    if not (isinstance(k, torch.Tensor) and k.is_cuda):
-        raise TypeError("k_cache must be a CUDA tensor")
-    if not (isinstance(v, torch.Tensor) and v.is_cuda):
-        raise TypeError("v_cache must be a CUDA tensor")
-    shape, st = k.shape, k.stride()
-    if shape != v.shape or k.dtype != v.dtype or k.device != v.device or \
-            not (len(shape) == 4 or layered and len(shape) == 5):
-        raise ValueError("k_cache and v_cache must be [num_pages, page_size, heads, head_dim] of "
-                         "one shape, type and device")
-    if st != v.stride() or (st[-1] != 1 and shape[-1] > 1):
-        raise ValueError("k_cache and v_cache must have the same strides and dense rows")
-    c = sv_kv_cache(k.data_ptr(), v.data_ptr(), _dtype_code(k), *shape[-4:], *st[-4:-1])
-    if not layered:
-        return c
-    return (c, shape[0], st[0]) if len(shape) == 5 else (c, 1, 0)
-
-
-def _token_rows(t: torch.Tensor, name: str, cache: torch.Tensor, heads: int | None):
-    """Shape, batch stride and token stride of [B, n, heads, head_dim] with
-    dense tokens."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    shape = t.shape
-    if len(shape) != 4 or shape[3] != cache.shape[-1] or (heads and shape[2] != heads):
-        raise ValueError(f"{name} must be [B, n, heads, head_dim] matching the cache, got "
-                         f"{tuple(shape)}")
-    if t.dtype != cache.dtype or t.device != cache.device:
-        raise ValueError(f"{name} must have the cache's type and device")
-    st = t.stride()
-    if (shape[3] > 1 and st[3] != 1) or (shape[2] > 1 and st[2] != shape[3]):
-        raise ValueError(f"the heads of a token of {name} must be dense")
-    return shape, st[0], st[1]
+        r = fn(*args)
+    else:
+        if isinstance(args[0], torch.Tensor) and args[0].device != stream.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on "
+                             f"{args[0].device}")
+        with torch.cuda.stream(stream):
+            r = fn(*args)
+    if r.__class__ is int and r != SV_OK:
+        raise SVError(what, r)
+    return r
 
 
 def sv_kv_plan(kv_len: torch.Tensor, block_table: torch.Tensor, pages: torch.Tensor,
@@ -649,33 +597,9 @@ def sv_kv_plan(kv_len: torch.Tensor, block_table: torch.Tensor, pages: torch.Ten
     to slots (see sv.h).  block_table [B, max_pages] and free_pages change in
     place.  Returns kv_len, pages, free_count, q_len, slot_map and positions
     (allocated unless given in `out`, where the first four may be inputs)."""
-    _dev(kv_len, "kv_len", torch.int32)
-    dev = kv_len.device
-    B, i32 = kv_len.numel(), torch.int32
-    o = dict(out) if out else {}
-    if len(o) < 6:
-        for name, shape, dt in (("kv_len", (B,), i32), ("pages", (B,), i32),
-                                ("free_count", (1,), i32), ("q_len", (B,), i32),
-                                ("slot_map", (B, max_new), torch.int64),
-                                ("positions", (B, max_new), i32)):
-            if name not in o:
-                o[name] = _empty(shape, dt, dev, stream)
-    table, max_pages = _rows(block_table, "block_table", dev, B)
-    _dev(free_pages, "free_pages", i32)
-    num = free_pages.numel()
-    _launch(lib().sv_kv_plan, "sv_kv_plan", dev, stream, kv_len.data_ptr(),
-            _ptr(written, "written", i32, dev, B), _ptr(accepted_len, "accepted_len", i32, dev, B),
-            _ptr(release, "release", i32, dev, B), _ptr(new_len, "new_len", i32, dev, B), B,
-            max_new, page_size, num, table, max_pages, _ptr(pages, "pages", i32, dev, B),
-            _ptr(free_pages, "free_pages", i32, dev, num),
-            _ptr(free_count, "free_count", i32, dev, 1), _ptr(o["kv_len"], "kv_len", i32, dev, B),
-            _ptr(o["pages"], "pages", i32, dev, B),
-            _ptr(o["free_count"], "free_count", i32, dev, 1),
-            _ptr(o["q_len"], "q_len", i32, dev, B),
-            _ptr(o["slot_map"], "slot_map", torch.int64, dev, B * max_new),
-            _ptr(o["positions"], "positions", i32, dev, B * max_new),
-            _ptr(device_status, "device_status", i32, dev, 1))
-    return o
+    return _call("sv_kv_plan", _native().plan, stream, kv_len, block_table, pages, free_pages,
+                 free_count, new_len, max_new, page_size, written, accepted_len, release, out,
+                 device_status)
 
 
 def sv_kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cache: torch.Tensor,
@@ -684,27 +608,15 @@ def sv_kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cac
     """Write new tokens' keys and values [B, n, heads, head_dim] to their
     slots (slot_map [B, n] int64, negative: none) of the caches [num_pages,
     page_size, heads, head_dim] (see sv.h)."""
-    c = _kv_cache(k_cache, v_cache)
-    dev = k_cache.device
-    rows = _token_rows(k, "k", k_cache, c.heads)
-    if _token_rows(v, "v", k_cache, c.heads) != rows:
-        raise ValueError("k and v must have the same shape and strides")
-    (B, n, _, _), sb, st = rows
-    _launch(lib().sv_kv_append, "sv_kv_append", dev, stream, ctypes.byref(c), k.data_ptr(),
-            v.data_ptr(), B, n, sb, st, _ptr(slot_map, "slot_map", torch.int64, dev, B * n),
-            _ptr(device_status, "device_status", torch.int32, dev, 1))
-
-
-@functools.lru_cache(maxsize=None)  # of the sizes alone
-def _attend_scratch_size(n: int, q_heads: int, heads: int, head_dim: int, code: int) -> int:
-    return int(lib().sv_kv_attend_scratch_size(1, n, q_heads, heads, head_dim, code))
+    _call("sv_kv_append", _native().append, stream, k, v, slot_map, k_cache, v_cache,
+          device_status)
 
 
 def sv_kv_attend_scratch_size(B: int, n: int, q_heads: int, heads: int, head_dim: int,
                               dtype: torch.dtype) -> int:
     """Bytes of scratch that sv_kv_attend needs (the same for every B)."""
     code = SV_BF16 if dtype == torch.bfloat16 else SV_F32
-    return _attend_scratch_size(n, q_heads, heads, head_dim, code)
+    return int(lib().sv_kv_attend_scratch_size(B, n, q_heads, heads, head_dim, code))
 
 
 def sv_kv_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -718,25 +630,8 @@ def sv_kv_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     out [B, n, q_heads, head_dim] and lse [B, n, q_heads].  scale defaults to
     head_dim ** -0.5.  scratch: sv_kv_attend_scratch_size bytes for this call
     (torch's allocator gives them if it is None)."""
-    c = _kv_cache(k_cache, v_cache)
-    dev, i32 = k_cache.device, torch.int32
-    (B, n, hq, d), sb, st = _token_rows(q, "q", k_cache, None)
-    o = dict(out) if out else {}
-    if "out" not in o:
-        o["out"] = _empty((B, n, hq, d), q.dtype, dev, stream)
-    if "lse" not in o:
-        o["lse"] = _empty((B, n, hq), torch.float32, dev, stream)
-    if scratch is None:
-        scratch = _empty(_attend_scratch_size(n, hq, c.heads, d, c.dtype), torch.uint8, dev, stream)
-    table, max_pages = _rows(block_table, "block_table", dev, B)
-    _launch(lib().sv_kv_attend, "sv_kv_attend", dev, stream, ctypes.byref(c), q.data_ptr(), sb, st, B,
-            n, hq, table, max_pages, _ptr(kv_len, "kv_len", i32, dev, B),
-            _ptr(q_len, "q_len", i32, dev, B), _ptr(parents, "parents", i32, dev, B * n),
-            d ** -0.5 if scale is None else scale, _ptr(o["out"], "out", q.dtype, dev, B * n * hq * d),
-            _ptr(o["lse"], "lse", torch.float32, dev, B * n * hq),
-            _ptr(scratch, "scratch", torch.uint8, dev, scratch.numel()), scratch.numel(),
-            _ptr(device_status, "device_status", i32, dev, 1))
-    return o
+    return _call("sv_kv_attend", _native().attend, stream, q, k_cache, v_cache, block_table,
+                 kv_len, q_len, parents, scale, out, scratch, device_status)
 
 
 def sv_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -746,15 +641,5 @@ def sv_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torc
     Caches [num_pages, page_size, heads, head_dim] of one layer, or [layers,
     ...] of all of them; accepted_nodes [B, max_depth + 1] and accepted_len
     [B] as sv_verify_tree_* return them."""
-    c, layers, layer_stride = _kv_cache(k_cache, v_cache, True)
-    if layers == 0:
-        return
-    dev, i32 = k_cache.device, torch.int32
-    _dev(kv_len, "kv_len", i32)
-    B = kv_len.numel()
-    table, max_pages = _rows(block_table, "block_table", dev, B)
-    nodes, width = _rows(accepted_nodes, "accepted_nodes", dev, B)
-    _launch(lib().sv_kv_commit, "sv_kv_commit", dev, stream, ctypes.byref(c), layers, layer_stride,
-            B, table, max_pages, _ptr(kv_len, "kv_len", i32, dev, B), nodes, width,
-            _ptr(accepted_len, "accepted_len", i32, dev, B),
-            _ptr(device_status, "device_status", i32, dev, 1))
+    _call("sv_kv_commit", _native().commit, stream, k_cache, v_cache, block_table, kv_len,
+          accepted_nodes, accepted_len, device_status)
