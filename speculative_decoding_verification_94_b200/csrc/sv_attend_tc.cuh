@@ -152,8 +152,25 @@ __device__ __forceinline__ void tc_st(uint32_t a, const uint32_t (&r)[32]) {
                "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(a)
                : "memory");
 }
-__device__ __forceinline__ void tc_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// Waits for the loads so far; the values of `r` are not there before.
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -166,6 +183,12 @@ __device__ __forceinline__ void tma_page(void* dst, const CUtensorMap* map, int 
       "[%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
       "l"(map), "r"(smem_u32(bar)), "r"(col), "r"(token), "r"(head), "r"(page)
       : "memory");
+}
+// The largest of three; NaN only if all are.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 // Named barrier of the softmax threads.
 __device__ __forceinline__ void softmax_sync() {
@@ -478,23 +501,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                      ? att_tail_bits<32>(par, qi, pos0 + c * 32, kv, tree_ok)
                      : 0xffffffffu;
         };
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < kKeys / 32; ++c) {
-          uint32_t x[32];
-          tc_ld(mine + c * 32, x);
-          tc_wait_ld();
+        constexpr int kChunks = kKeys / 32;
+        auto hide = [&](int c, uint32_t (&x)[32]) {
           if (tail) {
             const uint32_t bits = seen(c);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!(bits >> e & 1u)) x[e] = 0xff800000u;
           }
+        };
+        // chunk c is looked at while chunk c + 1 is on its way
+        uint32_t x[2][32];
+        float top = -INFINITY;
+        tc_ld(mine, x[0]);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          tc_wait_ld(x[c & 1]);
+          if (c + 1 < kChunks) tc_ld(mine + (c + 1) * 32, x[(c + 1) & 1]);
+          hide(c, x[c & 1]);
           float t2[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 32; ++e) t2[e & 3] = fmaxf(t2[e & 3], __uint_as_float(x[e]));
+          for (int e = 0; e < 32; e += 2)
+            t2[(e >> 1) & 3] = max3(t2[(e >> 1) & 3], __uint_as_float(x[c & 1][e]),
+                                    __uint_as_float(x[c & 1][e + 1]));
           top = fmaxf(fmaxf(t2[0], t2[1]), fmaxf(t2[2], t2[3]));
         }
+        if (kChunks > 1) tc_ld(mine, x[0]);
         top *= p.scale_log2;  // scale > 0 here
         // a new maximum only when weights would pass 2^8
         const bool grow = top > m + 8.f || (m == -INFINITY && top != -INFINITY);
@@ -510,7 +542,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int c = 0; c < D; c += 32) {
             uint32_t y[32];
             tc_ld(o_at + c, y);
-            tc_wait_ld();
+            tc_wait_ld(y);
 #pragma unroll
             for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * a);
             tc_st(o_at + c, y);
@@ -522,30 +554,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         const float ms = m == -INFINITY ? 0.f : m;
         const unsigned long long cc = f2_pack(p.scale_log2, p.scale_log2), mm = f2_pack(-ms, -ms);
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        unsigned long long sum[2] = {0, 0};
         // P over S: bf16 pairs in the first half of their keys' columns
-#pragma unroll 1
-        for (int c = 0; c < kKeys / 32; ++c) {
-          uint32_t x[32];
-          tc_ld(mine + c * 32, x);
-          tc_wait_ld();
-          if (tail) {
-            const uint32_t bits = seen(c);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(bits >> e & 1u)) x[e] = 0xff800000u;
+        for (int c = 0; c < kChunks; ++c) {
+          if (kChunks > 1) {
+            tc_wait_ld(x[c & 1]);
+            if (c + 1 < kChunks) tc_ld(mine + (c + 1) * 32, x[(c + 1) & 1]);
+            hide(c, x[c & 1]);
           }
           uint32_t y[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float a, b;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), cc,
-                             mm),
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c & 1][2 * e]),
+                                     __uint_as_float(x[c & 1][2 * e + 1])),
+                             cc, mm),
                       a, b);
             a = pow2(a);
             b = pow2(b);
-            sum[e & 1] += a;
-            sum[2 + (e & 1)] += b;
+            sum[e & 1] = f2_add(sum[e & 1], f2_pack(a, b));
             y[e] = pack_bf16(a, b);
           }
           tc_st(mine + c * 32, y);
@@ -556,7 +584,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int c = 0; c < 4; ++c)
             if (c / (kKeys / 32) != copy) tc_st(s_at + c * 32, zero);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float s0, s1;
+        f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
         if (tail) {
           // Values past the end become zeros, and so do new tokens' values
           // that are not finite: as 0 x inf they would reach rows that do not
@@ -668,7 +698,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if constexpr (C::kCols == 32) {
             uint32_t y[32];
             tc_ld(o_at + c0, y);
-            tc_wait_ld();
+            tc_wait_ld(y);
 #pragma unroll
             for (int j = 0; j < kPieces; ++j)
               dst[j ^ (lr & (kPieces - 1))] = make_float4(
@@ -677,7 +707,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           } else {
             uint32_t y[16];
             tc_ld(o_at + c0, y);
-            tc_wait_ld();
+            tc_wait_ld(y);
 #pragma unroll
             for (int j = 0; j < kPieces; ++j)
               dst[j ^ (lr & (kPieces - 1))] = make_float4(
