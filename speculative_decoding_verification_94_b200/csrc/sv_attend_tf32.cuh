@@ -2,7 +2,7 @@
 // head sizes 64 and 128.
 //
 // From 16 rows on the fp32 pipe is the bound by far (32 requests of 4000 keys,
-// 16 rows: 680 us against 163 us for the read).  Here the products go
+// 16 rows: 680 us against 163 us for the read; this kernel 280).  Here the products go
 // through the tensor cores in tf32, which has 11 bits: each operand is the
 // sum of two tf32 numbers, x = h + l, and a product is three, h h' + h l' + l h'.
 // Weights and q round h to nearest (|l| <= 2^-11 |x|), keys and values cut
@@ -58,6 +58,18 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A B alone.  The tensor core cuts its sums off, which adds up over thousands
+// of steps (60,000 keys: an error of 1.7e-5 of the output, 1.5e-6 without): a
+// step's product, and every four of a score, are added by fp32 additions.
+__device__ __forceinline__ void mma_tf32_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 template <int D>
@@ -161,7 +173,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_tf32_kernel(const Atten
       const uint32_t ka = smem_u32(kt);
       bad |= (bad_stages >> stage) & 1u;
       // scores: rows lane / 4 and + 8, keys 2 (lane % 4) and + 1
-      float z[4] = {0.f, 0.f, 0.f, 0.f}, zl[4] = {0.f, 0.f, 0.f, 0.f};
+      float z[4] = {0.f, 0.f, 0.f, 0.f}, zl[4] = {0.f, 0.f, 0.f, 0.f}, z4[4];
       {
         const uint32_t krow = ka + (lane & 7) * C::kRowBytes;
         const int qr = lane & 15;
@@ -178,9 +190,16 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_tf32_kernel(const Atten
             ldmatrix4(at + C::kQ, ql);
             cut_tf32(__uint_as_float(kf[2 * j]), h0, l0);
             cut_tf32(__uint_as_float(kf[2 * j + 1]), h1, l1);
-            mma_tf32(z, qh, h0, h1);
+            if (ks % 4 == 0 && j == 0)
+              mma_tf32_first(z4, qh, h0, h1);
+            else
+              mma_tf32(z4, qh, h0, h1);
             mma_tf32(zl, qh, l0, l1);
             mma_tf32(zl, ql, h0, h1);
+          }
+          if (ks % 4 == 2) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] += z4[e];
           }
         }
       }
@@ -275,9 +294,12 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_tf32_kernel(const Atten
           uint32_t h0, l0, h1, l1;
           cut_tf32(v0[((c ^ k0) << 2) + (g & 3)], h0, l0);
           cut_tf32(v1[((c ^ (k0 + 1)) << 2) + (g & 3)], h1, l1);
-          mma_tf32(o[0][nt], pl, h0, h1);
-          mma_tf32(o[0][nt], ph, l0, l1);
-          mma_tf32(o[0][nt], ph, h0, h1);
+          float c4[4];
+          mma_tf32_first(c4, pl, h0, h1);
+          mma_tf32(c4, ph, l0, l1);
+          mma_tf32(c4, ph, h0, h1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[0][nt][e] += c4[e];
         }
       }
       __syncwarp();

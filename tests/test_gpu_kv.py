@@ -509,6 +509,33 @@ def test_attend_offsets_past_32_bits():
     assert torch.equal(k[2, 5], x[0, 0]) and torch.equal(v[2, 5], x[0, 0])
 
 
+@pytest.mark.parametrize("n,g", [(1, 4), (2, 4), (4, 4)])
+def test_attend_fp32_sums_do_not_drift(n, g):
+    """Blocks that add up 250 steps of keys: roundings to nearest, independent,
+    give an error of about sqrt(250) 2^-24 of the output, with the products' 20
+    2^-24 below 2e-6; sums that are cut off would give 250 * 2^-24 / 2 and more,
+    7e-6 (the norm of the error against the norm of the output)."""
+    B, L, hkv, d = 64, 8000, 4, 64
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    k = torch.randn(B * L // 16, 16, hkv, d, generator=gen, device=DEV)
+    v = torch.rand(k.shape, generator=gen, device=DEV)  # of one sign
+    q = torch.randn(B, n, hkv * g, d, generator=gen, device=DEV)
+    table = torch.arange(B * L // 16, device=DEV, dtype=torch.int32).view(B, -1)
+    o = sv.sv_kv_attend(q, k, v, table, i32([L - n] * B))["out"]
+    err = ref2 = 0.0
+    for b in (0, 31, 63):
+        kk, vv = (x.view(B, L, hkv, d)[b].double().transpose(0, 1) for x in (k, v))
+        qq = q[b].double().view(n, hkv, g, d).permute(1, 0, 2, 3).reshape(hkv, n * g, d)
+        z = qq @ kk.transpose(1, 2) * d ** -0.5
+        keep = torch.arange(L, device=DEV)[None, :] <= L - n + torch.arange(
+            n, device=DEV).repeat_interleave(g)[:, None]
+        r = torch.softmax(torch.where(keep, z, float("-inf")), -1) @ vv
+        r = r.view(hkv, n, g, d).permute(1, 0, 2, 3).reshape(n, hkv * g, d)
+        err += float(((o[b].double() - r) ** 2).sum())
+        ref2 += float((r ** 2).sum())
+    assert (err / ref2) ** 0.5 < 2e-6
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attend_repeats_bit_for_bit_whatever_its_scratch_holds(dtype):
     dt = torch.bfloat16 if dtype == "bf16" else torch.float32
