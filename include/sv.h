@@ -482,7 +482,9 @@ SV_API sv_status sv_kv_append(const sv_kv_cache* cache, const void* k, const voi
  *   or NULL.
  *   block_table [B, max_pages], kv_len [B]; q_len [B] or NULL (n everywhere);
  *   parents [B, n] or NULL: int32.
- *   1 <= n <= 1024, q_heads a multiple of heads, scale finite.
+ *   1 <= n <= 1024, q_heads a multiple of heads, scale finite.  A longer
+ *   prompt is attended in pieces: after all of it was appended, piece p is a
+ *   call with kv_len + 1024 p.
  *   A request with lengths out of range sets SV_DEV_BAD_LEN, a row whose keys
  *   are on a page outside [0, num_pages) SV_DEV_BAD_INDEX, a row with a bad
  *   parent on its way up SV_DEV_BAD_TREE; their outputs are NaN (with

@@ -509,6 +509,96 @@ def test_attend_offsets_past_32_bits():
     assert torch.equal(k[2, 5], x[0, 0]) and torch.equal(v[2, 5], x[0, 0])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", ["chain", "line", "bush"])
+def test_attend_the_largest_step(dtype, shape):
+    """1024 new tokens: a chain, the same as a tree of one line (the longest
+    walks up), and a bush."""
+    s = scenario(1, 1024, 2, 1, 64, 16, [70], dtype, seed=41)
+    if shape == "line":
+        s["parents"] = [[j - 1 for j in range(1024)]]
+    elif shape == "bush":
+        s["parents"] = [[-1] + [j // 3 if j % 7 else j - 1 for j in range(1, 1024)]]
+    out, lse, st = call_attend(s)
+    assert st == 0
+    check_attend(s, out, lse)
+
+
+def test_attend_a_prompt_in_pieces():
+    """Pieces of a prompt, each over the whole of what stands before it, equal
+    to rounding what one token at a time gives."""
+    s = scenario(2, 300, 8, 2, 64, 16, [0, 33], "bf16", seed=43)
+    whole, lw, _ = call_attend(s)
+    for n, at in ((128, 0), (128, 128), (44, 256), (1, 299)):
+        t = dict(s, q=s["q"][:, at:at + n], q_len=[n, n], kv_len=[x + at for x in s["kv_len"]])
+        out, lse, st = call_attend(t)
+        assert st == 0
+        check_attend(t, out, lse)
+        assert ((lse - lw[:, at:at + n]).abs() <= 1e-5 * (1 + lse.abs())).all()
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_a_step_captured_and_replayed(side):
+    """plan, append, attend and commit in one graph, state in place: five
+    replays leave the bits of five steps without a graph; on a side stream too."""
+    B, n, page, mp, num = 6, 6, 4, 30, 200
+    par = i32([[-1, 0, 0, 1, 1, 2]] * B)
+
+    def fresh():
+        g = torch.Generator(device=DEV).manual_seed(5)
+        kc, vc = make_cache(num, page, 2, 64, torch.bfloat16, "dense", 7)
+        x = torch.randn(B, n, 12, 64, generator=g, device=DEV).bfloat16()
+        return dict(kv_len=i32([3, 0, 9, 4, 1, 7]), pages=i32([1, 0, 3, 1, 1, 2]),
+                    count=i32([num - 8]), written=i32([0] * B), free=i32(
+                        list(range(8, num)) + [-1] * 8),
+                    table=i32([r + [-1] * (mp - len(r)) for r in (
+                        [0], [], [1, 2, 3], [4], [5], [6, 7])]),
+                    acc=i32([2, 1, 0, 2, 1, 0]), new=i32([6, 6, 1, 6, 3, 0]),
+                    nodes=i32([[0, 2, 5], [0, 1, -1], [0, -1, -1], [0, 1, 4], [0, 2, -1],
+                               [0, -1, -1]]), x=x, kc=kc, vc=vc, st=status())
+
+    def step(s, stream=None):
+        o = sv.sv_kv_plan(s["kv_len"], s["table"], s["pages"], s["free"], s["count"], s["new"], n,
+                          page, written=s["written"], accepted_len=s["acc"], stream=stream,
+                          out=dict(kv_len=s["kv_len"], pages=s["pages"], free_count=s["count"],
+                                   q_len=s["written"]), device_status=s["st"])
+        sv.sv_kv_append(s["x"][:, :, 8:10], s["x"][:, :, 10:], o["slot_map"], s["kc"], s["vc"],
+                        device_status=s["st"], stream=stream)
+        a = sv.sv_kv_attend(s["x"][:, :, :8], s["kc"], s["vc"], s["table"], s["kv_len"],
+                            q_len=s["written"], parents=par, device_status=s["st"], stream=stream)
+        s["x"].copy_(torch.cat([a["out"], s["x"][:, :, :4]], 2))  # the next step's inputs
+        sv.sv_kv_commit(s["kc"], s["vc"], s["table"], s["kv_len"], s["nodes"], s["acc"],
+                        device_status=s["st"], stream=stream)
+
+    want, got = fresh(), fresh()
+    # tokens 0 .. accepted of a request that writes fewer are the last step's
+    for s in (want, got):
+        s["acc"].copy_(torch.minimum(s["acc"], (s["new"] - 1).clamp(min=0)))
+    stream = torch.cuda.Stream()
+    for _ in range(5):
+        if side:
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                step(want, stream)
+            torch.cuda.current_stream().wait_stream(stream)
+        else:
+            step(want)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    state = {k: v.clone() for k, v in got.items()}
+    with torch.cuda.graph(g):
+        step(got)
+    for k, v in state.items():
+        got[k].copy_(v)
+    for _ in range(5):
+        g.replay()
+    torch.cuda.synchronize()
+    assert int(want["st"].item()) == 0
+    for k in want:
+        bits = torch.int16 if want[k].dtype == torch.bfloat16 else want[k].dtype
+        assert torch.equal(want[k].view(bits), got[k].view(bits)), k
+
+
 @pytest.mark.parametrize("n,g", [(1, 4), (2, 4), (4, 4)])
 def test_attend_fp32_sums_do_not_drift(n, g):
     """Blocks that add up 250 steps of keys: roundings to nearest, independent,
