@@ -20,7 +20,7 @@
 // 0.0021 of its size.
 //
 // Measured: 256 requests of 100 to 4000 tokens, 8 key heads, 4 rows: 2.19 GB
-// in 350 us, 6.3 TB/s.  At 16 rows and 32 requests of 700 to 9000 tokens this
+// in 332 us, 6.6 TB/s.  At 16 rows and 32 requests of 700 to 9000 tokens this
 // kernel and the tensor-memory one both take 65 us, at 28 rows 106 against
 // 70 us; with 256 requests of 100 to 300 tokens 53 against 82 us at 16 rows.
 #pragma once
@@ -29,7 +29,9 @@
 
 namespace sv {
 
-constexpr int kMmaOv = 1;
+// What a segment costs beside its tiles, in tiles (256 requests of 100 to 4000
+// tokens: 358 us with 0, 338 with 1, 332 with 2 and with 4).
+constexpr int kMmaOv = 2;
 constexpr int kMmaThreads = 128, kMmaWarps = 4, kMmaKeys = 16, kMmaU = kMmaWarps * kMmaKeys;
 
 template <int D, int MT>

@@ -42,7 +42,9 @@ namespace sv {
 
 constexpr int kTcU = 128;            // keys of a tile
 // A segment's beginning and end, in tiles: about 5 us with 32 rows, 10 us with 128.
-__host__ __device__ constexpr int tc_ov(int rt) { return rt == 128 ? 7 : rt == 64 ? 4 : 3; }
+// (With 2, 3 and 5 instead, 8 requests of 28 rows took 31 us instead of 25, the
+// 32 requests of 28 rows 74 us instead of 68; with 5, 6 and 12 as now.)
+__host__ __device__ constexpr int tc_ov(int rt) { return rt == 128 ? 9 : rt == 64 ? 5 : 4; }
 constexpr int kTcSoftmax = 256;      // threads of the two warp groups
 constexpr int kTcThreads = 384;      // + two copy warps, product warp, one for the rest
 constexpr int kTcStages = 3;
