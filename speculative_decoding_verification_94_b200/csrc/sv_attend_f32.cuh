@@ -1,4 +1,5 @@
-// sv_attend_f32.cuh -- fp32 attention of head sizes 64 and 128, up to 8 rows.
+// sv_attend_f32.cuh -- fp32 attention of head sizes up to 128 (D is 64 or 128, the
+// columns past the head size are zeros), up to 8 rows.
 //
 // A key costs 4 D rows operations against 8 D bytes: up to about 8 rows the
 // read of the cache is the bound (32 requests of 4000 keys, 8 key heads, 4
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_f32_kernel(const Attend
       for (int j = 0; j < kF32Keys / kPerCopy; ++j) {
         const int row = j * kPerCopy + lane / kChunks;
         const long long o = __shfl_sync(0xffffffffu, at, row);
-        const bool on = o >= 0;
+        const bool on = o >= 0 && c * 4 < p.d;
         const long long src = on ? o + c * 4 : 0;
         const uint32_t to = dst + row * C::kRowBytes + ((c ^ ((row & 1) << 2)) << 4);
         cp_async16(to, kc + src, on);
@@ -119,10 +120,10 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_f32_kernel(const Attend
     for (int e = tid; e < RT * D; e += kF32Threads) {
       const int r = e / D, d = e % D;
       float x = 0.f;
-      if (r < rows) {
+      if (r < rows && d < p.d) {
         const int i = fast_div(row0 + r, p.div_g), gi = (row0 + r) - i * p.g;
         x = static_cast<const float*>(p.q)[cur.b * p.q_b + i * p.q_t +
-                                           (long long)(h * p.g + gi) * D + d];
+                                           (long long)(h * p.g + gi) * p.d + d];
       }
       s_q[e] = x;
     }
@@ -311,8 +312,9 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_f32_kernel(const Attend
         }
         if (whole) {
           const long long o = att_out_row(p, cur.b, h, row0 + row);
-          reinterpret_cast<float4*>(static_cast<float*>(p.out) + o * D)[c] =
-              make_float4(a.x / sum, a.y / sum, a.z / sum, a.w / sum);
+          if (c * 4 < p.d)
+            reinterpret_cast<float4*>(static_cast<float*>(p.out) + o * p.d)[c] =
+                make_float4(a.x / sum, a.y / sum, a.z / sum, a.w / sum);
           if (c == 0 && p.lse) p.lse[o] = (top + log2f(sum)) * kLn2;
         } else {
           __stcg(reinterpret_cast<float4*>(part + row * D) + c, a);

@@ -1,7 +1,8 @@
 // sv_attend_mma.cuh -- bf16 attention of few rows: one new token or a short
 // chain, up to 16 rows (new tokens x query heads per key head) at a time, and
 // up to 32 where the tensor-memory kernel does not take the call (pages that no
-// tile is a multiple of, unaligned q, a scale that is not positive).
+// tile is a multiple of, unaligned q, a scale that is not positive).  D is 64 or
+// 128; the columns past a smaller head size are zeros that are never loaded.
 //
 // With so few rows each key and value byte is used about once, so the bound
 // is the read of the cache: 4 D bytes of HBM per key against 4 D rows
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
       for (int j = 0; j < kMmaKeys / kPerCopy; ++j) {
         const int row = j * kPerCopy + lane / kChunks;
         const long long o = __shfl_sync(0xffffffffu, at, row);
-        const bool on = o >= 0;
+        const bool on = o >= 0 && c * 8 < p.d;
         const long long src = on ? o + c * 8 : 0;
         const uint32_t to = dst + row * C::kRowBytes + ((c ^ (row & 7)) << 4);
         cp_async16(to, kc + src, on);
@@ -191,11 +192,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
         const int i = on ? fast_div(r, p.div_g) : 0, gi = on ? r - i * p.g : 0;
         const uint32_t* src = reinterpret_cast<const uint32_t*>(
             static_cast<const __nv_bfloat16*>(p.q) + cur.b * p.q_b + i * p.q_t +
-            (long long)(h * p.g + gi) * D + (lane & 3) * 2);
+            (long long)(h * p.g + gi) * p.d + (lane & 3) * 2);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          qa[mt][ks][half] = on ? __ldg(src + ks * 8) : 0u;
-          qa[mt][ks][half + 2] = on ? __ldg(src + ks * 8 + 4) : 0u;
+          qa[mt][ks][half] = on && ks * 16 < p.d ? __ldg(src + ks * 8) : 0u;
+          qa[mt][ks][half + 2] = on && ks * 16 + 8 < p.d ? __ldg(src + ks * 8 + 4) : 0u;
         }
       }
     float o[MT][D / 8][4];
@@ -439,7 +440,9 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
           y.y = pack_bf16(x[2] * inv, x[3] * inv);
           y.z = pack_bf16(x[4] * inv, x[5] * inv);
           y.w = pack_bf16(x[6] * inv, x[7] * inv);
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow_at * D + c0 + ocol) = y;
+          if (c0 + ocol < p.d)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow_at * p.d + c0 +
+                                      ocol) = y;
         } else {
           float4* dst = reinterpret_cast<float4*>(part + orow * D + c0 + ocol);
           __stcg(dst, make_float4(x[0], x[1], x[2], x[3]));

@@ -1,5 +1,6 @@
 // sv_attend_tc.cuh -- bf16 attention of many rows (long drafts, candidate
-// trees) on the fifth-generation tensor cores.
+// trees) on the fifth-generation tensor cores.  D is 64 or 128; the tensor maps
+// fill the columns past a smaller head size with zeros.
 //
 // Products.  A tile is 128 keys.  S = Q K^T is one 128 x 128 product (128
 // lanes of tensor memory), O += P V one of 128 x D; their operands come from
@@ -436,8 +437,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int i = on ? fast_div(qr, p.div_g) : 0, gi = on ? qr - i * p.g : 0;
         const uint4* src = reinterpret_cast<const uint4*>(
             static_cast<const __nv_bfloat16*>(p.q) + c.b * p.q_b + i * p.q_t +
-            (long long)(h * p.g + gi) * D);
-        qx[j] = on ? __ldg(src + tid % kPieces16) : make_uint4(0, 0, 0, 0);
+            (long long)(h * p.g + gi) * p.d);
+        qx[j] = on && tid % kPieces16 * 8 < p.d ? __ldg(src + tid % kPieces16)
+                                                : make_uint4(0, 0, 0, 0);
       }
     };
     // ahead of its segment where that takes few registers
@@ -476,11 +478,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!kQAhead && next.v < s.u1) {
         const int h2 = next.seg / next.mt;
         const int qr = (next.seg - h2 * next.mt) * RT + (tid & (RT - 1));
-        if (qr < next.q * p.g && tid / RT * 64 < D) {
+        if (qr < next.q * p.g && tid / RT * 64 < p.d) {
           const int i = fast_div(qr, p.div_g), gi = qr - i * p.g;
           asm volatile("prefetch.global.L2 [%0];" ::"l"(
               static_cast<const __nv_bfloat16*>(p.q) + next.b * p.q_b + i * p.q_t +
-              (long long)(h2 * p.g + gi) * D + tid / RT * 64));
+              (long long)(h2 * p.g + gi) * p.d + tid / RT * 64));
         }
       }
       const int qi = min(fast_div(row0 + row, p.div_g), cur.q - 1);
@@ -690,7 +692,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           float rt, rs;
           row_stats(r, rt, rs);
           inv[i] = 1.f / rs;
-          out_at[i] = whole ? att_out_row(p, cur.b, h, row0 + r) * D : (long long)r * D;
+          out_at[i] = whole ? att_out_row(p, cur.b, h, row0 + r) * p.d : (long long)r * D;
         }
       }
 #pragma unroll 1
@@ -734,7 +736,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
           }
           const int col = c0 + j * 4;
-          if (fix) {
+          if (whole && col >= p.d) continue;
+          if (fix && col < p.d) {
             const int i = fast_div(row0 + r, p.div_g);
             for (int t = max(0, tile0 * kTcU - kv); t < cur.q; ++t) {
               const int pos = kv + t;

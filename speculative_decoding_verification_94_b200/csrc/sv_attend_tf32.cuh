@@ -1,5 +1,6 @@
 // sv_attend_tf32.cuh -- fp32 attention of more than 8 rows, 16 at a time, for
-// head sizes 64 and 128.
+// head sizes up to 128 (D is 64 or 128, the columns past the head size are
+// zeros).
 //
 // From 16 rows on the fp32 pipe is the bound by far (32 requests of 4000 keys,
 // 16 rows: 680 us against 163 us for the read; this kernel 280).  Here the products go
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_tf32_kernel(const Atten
       for (int j = 0; j < kF32Keys / kPerCopy; ++j) {
         const int row = j * kPerCopy + lane / kChunks;
         const long long o = __shfl_sync(0xffffffffu, at, row);
-        const bool on = o >= 0;
+        const bool on = o >= 0 && c * 4 < p.d;
         const long long src = on ? o + c * 4 : 0;
         const uint32_t to = dst + row * C::kRowBytes + ((c ^ (row & 7)) << 4);
         cp_async16(to, kc + src, on);
@@ -144,10 +145,10 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_tf32_kernel(const Atten
     for (int e = tid; e < kRows * D; e += kF32Threads) {
       const int r = e / D, d = e % D;
       float x = 0.f;
-      if (r < rows) {
+      if (r < rows && d < p.d) {
         const int i = fast_div(row0 + r, p.div_g), gi = (row0 + r) - i * p.g;
         x = static_cast<const float*>(p.q)[cur.b * p.q_b + i * p.q_t +
-                                           (long long)(h * p.g + gi) * D + d];
+                                           (long long)(h * p.g + gi) * p.d + d];
       }
       uint32_t hi, lo;
       split_tf32(x, hi, lo);
@@ -380,9 +381,11 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_tf32_kernel(const Atten
       if (orow < rows) {
         if (whole) {
           const float inv = 1.f / sum;
-          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow_at * D + c0 + ocol);
-          dst[0] = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-          dst[1] = make_float4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+          float4* dst =
+              reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow_at * p.d + c0 + ocol);
+          if (c0 + ocol < p.d) dst[0] = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+          if (c0 + ocol + 4 < p.d)
+            dst[1] = make_float4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
         } else {
           float4* dst = reinterpret_cast<float4*>(part + orow * D + c0 + ocol);
           __stcg(dst, make_float4(x[0], x[1], x[2], x[3]));

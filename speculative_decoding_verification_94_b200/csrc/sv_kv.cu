@@ -93,7 +93,7 @@ constexpr size_t kSharedBytes = (sizeof(AttShared) * kAttMaxBlocks + 255) / 256 
 // Rows of a row tile, which set the size of a partial result.  16 also covers
 // the general kernel, which any bf16 call may need for its strides.
 int tile_rows(int rows, int head_dim, sv_dtype dt) {
-  if (dt != SV_BF16 || (head_dim != 64 && head_dim != 128) || rows <= 16) return 16;
+  if (dt != SV_BF16 || head_dim > 128 || rows <= 16) return 16;
   return rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
 
@@ -438,20 +438,20 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_st
   // against 70, and with short contexts the kernel of few rows wins up to 16.
   const int box = tc_box(p.page);
   CUtensorMap km, vm;
-  if (cache->dtype == SV_BF16 && vec && aligned(out, 16) && (p.d == 64 || p.d == 128) &&
-      p.n * p.g > 16 && box && scale > 0.f &&
+  if (cache->dtype == SV_BF16 && vec && aligned(out, 16) && p.d <= 128 && p.n * p.g > 16 && box &&
+      scale > 0.f &&
       common_width({addr(q), p.q_b * es, p.q_t * es}) == 16 && tc_map(p, p.k, box, &km) &&
       tc_map(p, p.v, box, &vm)) {
     const long long wait = knob(SV_KNOB_WAIT_NS);
     const TcParams tp = {p, box, wait > 0 ? (unsigned long long)wait : kWaitLimitNs,
                          knob(SV_KNOB_STALL) != 0};
-    e = p.d == 128 ? launch_tc<128>(tp, km, vm, s) : launch_tc<64>(tp, km, vm, s);
-  } else if (cache->dtype == SV_BF16 && vec && pairs && p.d == 128)
+    e = p.d > 64 ? launch_tc<128>(tp, km, vm, s) : launch_tc<64>(tp, km, vm, s);
+  } else if (cache->dtype == SV_BF16 && vec && pairs && p.d > 64 && p.d <= 128)
     e = launch_mma<128>(p, s);
-  else if (cache->dtype == SV_BF16 && vec && pairs && p.d == 64)
+  else if (cache->dtype == SV_BF16 && vec && pairs && p.d <= 64)
     e = launch_mma<64>(p, s);
-  else if (cache->dtype == SV_F32 && vec && aligned(out, 16) && (p.d == 64 || p.d == 128))
-    e = p.d == 128 ? launch_f32<128>(p, s) : launch_f32<64>(p, s);
+  else if (cache->dtype == SV_F32 && vec && aligned(out, 16) && p.d <= 128)
+    e = p.d > 64 ? launch_f32<128>(p, s) : launch_f32<64>(p, s);
   else if (cache->dtype == SV_BF16)
     e = vec ? launch_general<__nv_bfloat16, true>(p, s) : launch_general<__nv_bfloat16, false>(p, s);
   else

@@ -227,8 +227,8 @@ def check_attend(s, out, lse, rows=None):
     as a sum of two bf16 they are off by 2^-16 up to 16 rows a key head, as
     one bf16 by half a step, 2^-8, beyond (sum |dp v| <= 2^-8 sum p |v|).  fp32
     products of more than 8 rows go through two-part tf32 and are off by 20 eps
-    each: 20 eps size of a score, within 2 (d + 4) eps size where d >= 64, and
-    20 eps of the numerator, counted for both types.  The output then rounds
+    each: 20 eps size of a score and 20 eps of the numerator, counted for both
+    types.  The output then rounds
     by half a step of its type."""
     ref, rl, size, absv = O.attend(host(s["q"]), host(s["kc"]), host(s["vc"]), s["table"],
                                    s["kv_len"], s["q_len"], s["parents"], s["scale"])
@@ -236,7 +236,7 @@ def check_attend(s, out, lse, rows=None):
     eps = 2.0 ** -24
     bf = s["q"].dtype == torch.bfloat16
     n_keys = np.array(s["kv_len"])[:, None, None] + s["q"].shape[1]
-    w = (2 * (d + 4) * size + n_keys + 6 * (n_keys / 16 + 2)) * eps
+    w = ((2 * (d + 4) + 20) * size + n_keys + 6 * (n_keys / 16 + 2)) * eps
     rows = s["q"].shape[1] * s["q"].shape[2] // s["kc"].shape[2]
     rel = 2 * w + 20 * eps + (0.0 if not bf else 2.0 ** -16 if rows <= 16 else 2.0 ** -8)
     tol = rel[..., None] * absv + (2.0 ** -8 if bf else 2.0 ** -24) * np.abs(ref) + 1e-37
@@ -277,6 +277,13 @@ CASES = [
     (2, 20, 16, 2, 64, 4, [100, 259]),      # and pages too small for a tile's boxes
     (2, 9, 8, 2, 128, 8, [100, 259]),       # 36 rows, the smallest pages that boxes take
     (2, 20, 16, 2, 128, 256, [100, 700]),   # pages larger than a tile
+    (2, 3, 8, 2, 40, 16, [33, 300]),        # head sizes inside a kernel's 64 or 128 columns
+    (2, 20, 8, 2, 40, 16, [33, 300]),
+    (2, 9, 8, 2, 112, 16, [33, 700]),
+    (2, 40, 8, 2, 72, 32, [33, 300]),
+    (2, 4, 8, 2, 8, 16, [33, 300]),
+    (2, 12, 8, 2, 8, 16, [33, 300]),
+    (2, 12, 8, 2, 100, 16, [33, 300]),      # 16-byte rows in fp32 only
 ]
 
 
