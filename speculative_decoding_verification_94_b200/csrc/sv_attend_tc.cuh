@@ -219,7 +219,8 @@ struct TcParams {
 };
 
 // Wait for phase `parity` of a barrier, giving up after `limit_ns`.
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity,
+                                        unsigned long long limit_ns) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
@@ -243,7 +244,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t *k_full = bars, *k_empty = bars + 3, *v_full = bars + 6, *v_empty = bars + 9,
-           *s_full = bars + 12, *p_ready = bars + 14, *pv_done = bars + 16, *q_full = bars + 18, *q_first = bars + 19;
+           *s_full = bars + 12, *p_ready = bars + 14, *pv_done = bars + 16, *q_full = bars + 18,
+           *q_first = bars + 19;
   int* misc = reinterpret_cast<int*>(smem + C::kOffMisc);
   volatile int* s_abort = misc;      // a wait ran out
   int* s_bad = misc + 1;             // the segment's keys are on a bad page
@@ -381,7 +383,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                   const uint32_t o = (ks / 4) * C::kHalf + (ks % 4) * 32;
-                  tc_mma_ss(tmem + w * 128, tc_desc(qa + o, 16), tc_desc(ka + o, 16), kIdQk, ks > 0);
+                  tc_mma_ss(tmem + w * 128, tc_desc(qa + o, 16), tc_desc(ka + o, 16), kIdQk,
+                            ks > 0);
                 }
                 tc_commit(s_full + w);
                 tc_commit(k_empty + slot);
@@ -604,7 +607,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           // Pages past the end were copied as zeros already.
           const int pos0v = (tile0 + k) * kTcU;
-          const long long page_end = (long long)(fast_div(len - 1, p.div_page) + 1) * p.page - pos0v;
+          const long long page_end =
+              (long long)(fast_div(len - 1, p.div_page) + 1) * p.page - pos0v;
           const int end = page_end < kTcU ? (int)page_end : kTcU;
           constexpr int kChunks = D / 8, kRowsPer = 32 / kChunks;
           for (int r = max((cur.q > 1 ? kv : len) - pos0v, 0) + quad * kRowsPer + lane / kChunks;

@@ -3,8 +3,8 @@
 // Argument marshalling only, as the ctypes binding of the other calls, but in
 // C++: these calls stand between the layers of a model, where looking at each
 // tensor from Python (5 to 8 us a call) took longer than most of the kernels:
-// plan 12.5 -> 4.6 us, append 9.7 -> 4.1 us.  Each function checks its tensors, runs on their device
-// and its current stream, and returns the status of the C call; `plan` and
+// plan 12.5 -> 4.6 us, append 9.7 -> 4.1 us.  Each function checks its tensors,
+// runs on their device and its current stream, and returns the status of the C call; `plan` and
 // `attend` return the dict of outputs instead where the status is SV_OK.
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -193,7 +193,8 @@ PyObject* do_plan(PyObject* const* a) {
 PyObject* do_append(PyObject* const* a) {
   enum { kK, kV, kSlots, kKc, kVc, kStatus };
   const Cache c = cache(a[kKc], a[kVc], false);
-  const at::Tensor &k = token_rows(a[kK], "k", c, c.c.heads), &v = token_rows(a[kV], "v", c, c.c.heads);
+  const at::Tensor& k = token_rows(a[kK], "k", c, c.c.heads);
+  const at::Tensor& v = token_rows(a[kV], "v", c, c.c.heads);
   if (k.sizes() != v.sizes() || k.strides() != v.strides())
     value_error("k and v must have the same shape and strides");
   const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.dev);

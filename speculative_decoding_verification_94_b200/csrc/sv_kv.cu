@@ -98,9 +98,9 @@ int tile_rows(int rows, int head_dim, sv_dtype dt) {
 }
 
 size_t attend_scratch(int rows, int head_dim, sv_dtype dt) {
-  return kSharedBytes + (size_t)kAttMaxBlocks * 2 *
-                             att_partial_floats(tile_rows(rows, head_dim, dt), padded_dim(head_dim)) *
-                             4;
+  const int tile = tile_rows(rows, head_dim, dt);
+  return kSharedBytes +
+         (size_t)kAttMaxBlocks * 2 * att_partial_floats(tile, padded_dim(head_dim)) * 4;
 }
 
 // The second launch.
@@ -453,7 +453,8 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t batch_st
   else if (cache->dtype == SV_F32 && vec && aligned(out, 16) && p.d <= 128)
     e = p.d > 64 ? launch_f32<128>(p, s) : launch_f32<64>(p, s);
   else if (cache->dtype == SV_BF16)
-    e = vec ? launch_general<__nv_bfloat16, true>(p, s) : launch_general<__nv_bfloat16, false>(p, s);
+    e = vec ? launch_general<__nv_bfloat16, true>(p, s)
+            : launch_general<__nv_bfloat16, false>(p, s);
   else
     e = vec ? launch_general<float, true>(p, s) : launch_general<float, false>(p, s);
   return cuda_status(e);

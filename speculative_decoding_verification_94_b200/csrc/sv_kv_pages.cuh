@@ -198,7 +198,8 @@ __global__ void __launch_bounds__(kPlanMaxThreads) kv_plan_kernel(const PlanPara
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = i0 + j * threads;
-        if (i < (int)give_all && (long long)count + i < p.num_pages) p.free_pages[count + i] = id[j];
+        if (i < (int)give_all && (long long)count + i < p.num_pages)
+          p.free_pages[count + i] = id[j];
       }
     }
     __syncthreads();

@@ -124,7 +124,7 @@ def make_cache(pages, page, heads, d, dtype, layout, seed, fill=None):
     if layout == "dense":
         return rnd(pages, page, heads, d), rnd(pages, page, heads, d)
     if layout == "heads_first":
-        return (rnd(pages, heads, page, d).transpose(1, 2), rnd(pages, heads, page, d).transpose(1, 2))
+        return tuple(rnd(pages, heads, page, d).transpose(1, 2) for _ in range(2))
     if layout == "joint":  # keys and values of a page in one block
         t = rnd(pages, 2, page, heads, d)
         return t[:, 0], t[:, 1]

@@ -86,7 +86,8 @@ def test_attend_validates(lib):
 
     def call(c=None, **kw):
         a = dict(q=F, bs=1024, ts=256, B=4, n=4, hq=4, table=F, max_pages=8, kv_len=F, q_len=F,
-                 parents=F, scale=0.125, out=F + 4096, lse=F, ws=F, wsb=big, status=None, stream=None)
+                 parents=F, scale=0.125, out=F + 4096, lse=F, ws=F, wsb=big, status=None,
+                 stream=None)
         a.update(kw)
         return lib.sv_kv_attend(ctypes.byref(c or cache()), *a.values())
     for kw in BAD_CACHES:
