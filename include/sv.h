@@ -494,7 +494,9 @@ SV_API sv_status sv_kv_append(const sv_kv_cache* cache, const void* k, const voi
  *   anything before the call and holds anything after it, so a buffer that is
  *   to serve as their workspace has to be zeroed again.
  * Two launches: the attention, and the join of sequences that several blocks
- * shared.  Sums and softmax statistics are fp32.  The split of a sequence over the
+ * shared.  Sums and softmax statistics are fp32, whatever the number of rows;
+ * bf16: weights enter their products to 2^-16 of each; fp32: a product is off
+ * by at most 20 half steps.  The split of a sequence over the
  * device's blocks depends on all lengths of the batch, so a request's last
  * bits can differ between batches; a repeated call gives the same bits.
  */

@@ -7,17 +7,26 @@
 // shared memory (TMA, 128-byte swizzle), the weights P from tensor memory.
 // The lanes are the rows of a row tile of RT = 32, 64 or 128; with fewer than
 // 128 rows they are repeated, and copy c of a row takes the weights of the
-// c-th part of the keys only (the others are zero), so that all four warps
-// of a warp group work on the softmax of every tile; the copies add up at the
-// end.
+// c-th part of the keys only, so that all four warps of a warp group work on
+// the softmax of every tile; the copies add up at the end.
+//
+// Weights.  A weight enters the product as the sum of two bf16, its rounding
+// and the rest's, which keeps it to 2^-16, as in the kernel of few rows: the
+// output's error is then its own rounding (0.0017 of its size; 0.0021 with one
+// bf16).  128 rows take two products for it (16 instructions a tile instead of
+// 8).  Repeated rows take none: copies c and c ^ 1 of a row are partners that
+// share a maximum, and the rests of one's part go to the other's lanes, which
+// had zeros there.  The partner computes those weights from its own lanes of S.
 //
 // Bound.  One SM's share of HBM brings the 64 KB of a tile in 1.5 us.  An
 // instruction of the products (16 of the summed index) took 95 cycles whether
-// it was 64 or 128 wide, so a tile's 16 take 0.8 us, whatever RT is, and a
-// softmax of 128 rows 0.9 us.  With the products and the softmax taken out,
-// the copies alone needed 109 us for 130,000 keys of 8 heads (40 rows), with
-// them 110 us.  What was slower: weights as the sum of two bf16 (24
-// instructions a tile: 120 us), and S in halves of 64 keys (32: 133 us).
+// it was 64 or 128 wide, so a tile's 16 take 0.8 us (24 with 128 rows: 1.2 us),
+// and a softmax of 128 rows 0.9 us without the rests.  With the products and the
+// softmax taken out, the copies alone needed 109 us for 130,000 keys of 8 heads
+// (40 rows).  What the rests cost, from L2: nothing with 28 rows (32 requests of
+// 700 to 9000 keys, 68 us), 96 -> 101 us with 40 (130,000 keys), 50 -> 61 us
+// with 256 (8 requests of 2000 to 8000 keys; 9 us of it in the softmax, 3 in the
+// products).  What was slower: S in halves of 64 keys (32 instructions a tile).
 //
 // Roles.  Two warps issue the copies (keys, values), one the products, as
 // their operands arrive, one fills the rows behind a request's own.  Two warp
@@ -25,9 +34,7 @@
 // and sum, so that one's softmax runs under the other's products, and neither
 // waits for the other.  O stays in tensor memory; it is rescaled only when the
 // maximum grows by more than 2^8 (a weight may then be up to 2^8, which costs
-// no precision: the sum is fp32).  P is stored over S, rounded to bf16: the
-// output's error is then 0.0021 of its size, 0.0017 of which is the output's
-// own rounding.
+// no precision: the sum is fp32).  P is stored over S.
 //
 // Every wait has a time limit; a block whose wait runs out gives NaN for its
 // segments, sets SV_DEV_TIMEOUT and goes on to the end.
@@ -236,6 +243,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   using C = TcCfg<D>;
   constexpr int kCopies = 128 / RT;          // copies of a row among the lanes
   constexpr int kKeys = kTcU / kCopies;      // keys of a copy
+  constexpr int kParts = kCopies == 1 ? 2 : 1;  // of the weights, one product after the other
   extern __shared__ __align__(1024) unsigned char smem[];
   const AttendParams& p = tp.a;
   const unsigned long long wait_ns = tp.wait_ns;
@@ -364,9 +372,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const uint32_t va = smem_u32(smem + C::kOffV + slot * C::kTile);
                 const uint32_t pa = tmem + w * 128, o = tmem + 256 + w * 128;
 #pragma unroll
-                for (int ks = 0; ks < kTcU / 16; ++ks)
-                  tc_mma_ts(o, pa + (ks / 2) * 32 + (ks & 1) * 8, tc_desc(va + ks * 2048, C::kHalf),
-                            kIdPv, np >= 2 || ks);
+                for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                  for (int ks = 0; ks < kTcU / 16; ++ks)
+                    tc_mma_ts(o, pa + (ks / 2) * 32 + part * 16 + (ks & 1) * 8,
+                              tc_desc(va + ks * 2048, C::kHalf), kIdPv, np >= 2 || part || ks);
                 tc_commit(pv_done + w);
                 tc_commit(v_empty + slot);
                 ++streams[w];
@@ -498,17 +508,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           break;
         }
         tc_fence_after();
-        const int pos0 = (tile0 + k) * kTcU + copy * kKeys;
         // S is read twice, 32 columns at a time, for the maximum and for the
         // weights: tensor memory is near, registers are not plenty.
-        const uint32_t mine = s_at + copy * kKeys;
+        // The chunks of this copy, then those of its partner, whose weights'
+        // rests go to this copy's lanes.
+        constexpr int kOwn = kKeys / 32, kChunks = kCopies > 1 ? 2 * kOwn : kOwn;
+        auto chunk = [&](int c) { return c < kOwn ? copy * kOwn + c : (copy ^ 1) * kOwn + c - kOwn; };
         const bool tail = (tile0 + k + 1) * kTcU > kv;
         auto seen = [&](int c) {  // which of chunk c's keys this row sees
-          return pos0 + c * 32 + 32 > kv
-                     ? att_tail_bits<32>(par, qi, pos0 + c * 32, kv, tree_ok)
-                     : 0xffffffffu;
+          const int pos0 = (tile0 + k) * kTcU + chunk(c) * 32;
+          return pos0 + 32 > kv ? att_tail_bits<32>(par, qi, pos0, kv, tree_ok) : 0xffffffffu;
         };
-        constexpr int kChunks = kKeys / 32;
         auto hide = [&](int c, uint32_t (&x)[32]) {
           if (tail) {
             const uint32_t bits = seen(c);
@@ -520,11 +530,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // chunk c is looked at while chunk c + 1 is on its way
         uint32_t x[2][32];
         float top = -INFINITY;
-        tc_ld(mine, x[0]);
+        tc_ld(s_at + chunk(0) * 32, x[0]);
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
           tc_wait_ld(x[c & 1]);
-          if (c + 1 < kChunks) tc_ld(mine + (c + 1) * 32, x[(c + 1) & 1]);
+          if (c + 1 < kChunks) tc_ld(s_at + chunk(c + 1) * 32, x[(c + 1) & 1]);
           hide(c, x[c & 1]);
           float t2[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -533,7 +543,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     __uint_as_float(x[c & 1][e + 1]));
           top = fmaxf(fmaxf(t2[0], t2[1]), fmaxf(t2[2], t2[3]));
         }
-        if (kChunks > 1) tc_ld(mine, x[0]);
+        if (kChunks > 2) tc_ld(s_at + chunk(0) * 32, x[0]);  // two are still there
         top *= p.scale_log2;  // scale > 0 here
         // a new maximum only when weights would pass 2^8
         const bool grow = top > m + 8.f || (m == -INFINITY && top != -INFINITY);
@@ -562,15 +572,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float ms = m == -INFINITY ? 0.f : m;
         const unsigned long long cc = f2_pack(p.scale_log2, p.scale_log2), mm = f2_pack(-ms, -ms);
         unsigned long long sum[2] = {0, 0};
-        // P over S: bf16 pairs in the first half of their keys' columns
+        // P over S: bf16 pairs in the first half of their keys' columns; the
+        // rests in the second half, or in the partner's lanes
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          if (kChunks > 1) {
+          if (kChunks > 2) {
             tc_wait_ld(x[c & 1]);
-            if (c + 1 < kChunks) tc_ld(mine + (c + 1) * 32, x[(c + 1) & 1]);
+            if (c + 1 < kChunks) tc_ld(s_at + chunk(c + 1) * 32, x[(c + 1) & 1]);
             hide(c, x[c & 1]);
           }
-          uint32_t y[16];
+          uint32_t y[16], rest[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float a, b;
@@ -580,16 +591,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                       a, b);
             a = pow2(a);
             b = pow2(b);
-            sum[e & 1] = f2_add(sum[e & 1], f2_pack(a, b));
+            if (c < kOwn) sum[e & 1] = f2_add(sum[e & 1], f2_pack(a, b));
             y[e] = pack_bf16(a, b);
+            if (kCopies == 1 || c >= kOwn)
+              rest[e] = pack_bf16(a - bf16_lo(y[e]), b - bf16_hi(y[e]));
           }
-          tc_st(mine + c * 32, y);
+          tc_st(s_at + chunk(c) * 32, c < kOwn ? y : rest);
+          if (kCopies == 1) tc_st(s_at + chunk(c) * 32 + 16, rest);
         }
-        if constexpr (kCopies > 1) {  // the other copies' keys
+        if constexpr (kCopies > 2) {  // the other copies' keys
           const uint32_t zero[16] = {};
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (c / (kKeys / 32) != copy) tc_st(s_at + c * 32, zero);
+            if ((c / kOwn) / 2 != copy / 2) tc_st(s_at + c * 32, zero);
         }
         float s0, s1;
         f2_unpack(f2_add(sum[0], sum[1]), s0, s1);

@@ -1,0 +1,61 @@
+"""What the header promises of the paged cache calls, beside the agreement with
+the oracle: precision of long contexts and of many rows, values that are not
+finite, requests that a step leaves out, bad page ids, limits of sizes."""
+import pytest
+import torch
+
+from speculative_decoding_verification_94_b200 import sv
+from tests.test_gpu_kv import DEV, call_attend, i32, scenario, status
+
+pytestmark = pytest.mark.gpu
+
+
+def exact(s):
+    """(out, lse) of a scenario in float64, and sum p |v|; zeros and -inf for
+    tokens behind a request's own."""
+    q, kc, vc, page = s["q"].double(), s["kc"], s["vc"], s["page"]
+    B, n, hq, d = q.shape
+    heads = kc.shape[2]
+    g = hq // heads
+    out, absv = torch.zeros_like(q), torch.zeros_like(q)
+    lse = torch.full((B, n, hq), float("-inf"), dtype=torch.float64, device=q.device)
+    for b in range(B):
+        a, m = s["kv_len"][b], s["q_len"][b]
+        if m == 0:
+            continue
+        keep = torch.ones(m, a + m, dtype=torch.bool)
+        for i in range(m):
+            keep[i, a:] = False
+            j = i
+            while j >= 0:
+                keep[i, a + j] = True
+                j = j - 1 if s["parents"] is None else s["parents"][b][j]
+        keep = keep.to(q.device).repeat_interleave(g, 0)
+        ids = torch.tensor(s["table"][b][:-(-(a + m) // page)], device=q.device)
+        for h in range(heads):
+            k = kc[ids, :, h].reshape(-1, d)[:a + m].double()
+            v = vc[ids, :, h].reshape(-1, d)[:a + m].double()
+            z = q[b, :m, h * g:(h + 1) * g].reshape(m * g, d) @ k.T * s["scale"]
+            z = torch.where(keep, z, float("-inf"))
+            w = torch.softmax(z, -1)
+            out[b, :m, h * g:(h + 1) * g] = (w @ v).view(m, g, d)
+            absv[b, :m, h * g:(h + 1) * g] = (w @ v.abs()).view(m, g, d)
+            lse[b, :m, h * g:(h + 1) * g] = torch.logsumexp(z, -1).view(m, g)
+    return out, lse, absv
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,g", [(4, 7), (8, 5), (16, 4), (16, 8), (32, 8)])
+def test_attend_bf16_errs_by_its_outputs_rounding_alone(n, g, d, tree):
+    """The weights enter the product as two bf16, to 2^-16 of each: with
+    sum p |v| some ten times an output's size that is 1.5e-4 of the output,
+    scores in fp32 add as much, and the output's own rounding 1.7e-3.  They add
+    up as squares to 2 % more than the rounding of the exact output; 5 % are
+    allowed.  (Weights of one bf16 would add another 1.3e-3: 27 % more.)"""
+    s = scenario(2, n, 2 * g, 2, d, 16, [700, 2500], "bf16", tree=tree, seed=3 * n + d)
+    out, lse, st = call_attend(s)
+    assert st == 0
+    ref = exact(s)[0]
+    least = float((ref.bfloat16().double() - ref).norm())
+    assert float((out.double() - ref).norm()) <= 1.05 * least
