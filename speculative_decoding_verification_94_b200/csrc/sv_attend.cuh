@@ -135,7 +135,8 @@ struct AttShare {
 };
 
 // Every block sums the units of all requests and finds its own run.  `scratch`
-// is kShareBytes of shared memory.
+// is kShareBytes of shared memory, read until every thread has returned: it is
+// written again after a barrier or not at all.
 constexpr int kShareBytes = 128;
 template <int THREADS, int U, int RT, int OV>
 __device__ __forceinline__ AttShare att_share(const AttendParams& p, AttCursor<U, RT, OV>& cur,

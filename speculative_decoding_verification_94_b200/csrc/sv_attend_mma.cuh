@@ -44,7 +44,10 @@ struct MmaCfg {
   static constexpr int kCols = 64 / MT;                    // output columns added at a time
   static constexpr int kRing = kMmaWarps * kStages * kStage;
   static constexpr int kMerge = kMmaWarps * kRows * kCols * 4;
-  static constexpr int kSmem = kRing + kMerge;  // two blocks an SM
+  // of its own: nothing holds a warp back between the division of the work and
+  // its first results, while others may still read their part of it
+  static constexpr int kShare = kRing + kMerge;
+  static constexpr int kSmem = kShare + kShareBytes;  // two blocks an SM
 };
 
 // 16 bytes, or zeros.
@@ -128,7 +131,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) attend_mma_kernel(const Attend
   if (tid == 0) att_clear_note(p);
   pdl_launch_dependents();
   AttCursor<kMmaU, kRows, kMmaOv> cur;
-  const AttShare s = att_share<kMmaThreads>(p, cur, merge);
+  const AttShare s = att_share<kMmaThreads>(p, cur, smem + C::kShare);
 
   // ---- the copies: they run kStages - 1 tiles ahead of the products ---------
   AttCursor<kMmaU, kRows, kMmaOv> ahead = cur;

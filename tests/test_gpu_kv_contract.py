@@ -59,3 +59,20 @@ def test_attend_bf16_errs_by_its_outputs_rounding_alone(n, g, d, tree):
     ref = exact(s)[0]
     least = float((ref.bfloat16().double() - ref).norm())
     assert float((out.double() - ref).norm()) <= 1.05 * least
+
+
+@pytest.mark.parametrize("n,hq,d", [(1, 1, 64), (1, 4, 128), (2, 8, 128), (5, 8, 64)])
+def test_attend_of_the_shortest_segments_repeats(n, hq, d):
+    """One to three keys a request, so that a block's warps end their first
+    segment as soon as they can: the same bits in every call, and right ones."""
+    s = scenario(600, n, hq, 1, d, 16, [0, 2, 1], "bf16", ragged=True, seed=n + d)
+    want = call_attend(s)
+    ref, lse, absv = exact(s)
+    # three keys: 2^-16 of the weights, scores and powers to 300 half steps of
+    # fp32 of a score's size (below 100), half a step of the output
+    tol = absv * (2.0 ** -16 + 2 * 300 * 100 * 2.0 ** -24) + 2.0 ** -8 * ref.abs() + 1e-30
+    assert want[2] == 0 and ((want[0].double() - ref).abs() <= tol).all()
+    args = (s["q"], s["kc"], s["vc"], i32(s["table"]), i32(s["kv_len"]))
+    for _ in range(200):
+        o = sv.sv_kv_attend(*args, q_len=i32(s["q_len"]), scale=s["scale"])
+        assert torch.equal(o["out"], want[0]) and torch.equal(o["lse"], want[1])
