@@ -386,7 +386,9 @@ SV_API sv_status sv_kd_grad(const float* topk_logp, const int32_t* topk_idx, int
  * and after verification the next plan commits the accepted ones:
  *
  *   sv_kv_plan -> (projections) -> sv_kv_append -> sv_kv_attend -> (logits)
- *     -> sv_verify_chain_ragged or sv_verify_tree_* -> [sv_kv_commit] -> sv_kv_plan ...
+ *     -> sv_verify_chain_ragged or sv_verify_tree_* -> [sv_kv_commit_ragged] -> sv_kv_plan ...
+ *
+ * (sv_verify_chain_ragged with active = q_len and draft_len = max(q_len - 1, 0)).
  *
  * Pages of different requests, and of one request's table, are distinct
  * wherever a call writes; sv_kv_attend also reads shared ones.
@@ -522,11 +524,27 @@ SV_API sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t b
  *   outside the table or accepted_len >= width SV_DEV_BAD_LEN, a bad page
  *   SV_DEV_BAD_INDEX; such a request's cache is left as it is.
  *   0 <= B <= 65535.  No workspace.
+ *
+ * sv_kv_commit_ragged -- the same for a step that not every request took part
+ * in with all n nodes: q_len [B] as sv_kv_plan gives it.  The tree calls
+ * verify every row they are given, so a request that the plan left out
+ * (released, or out of pages) also has an accepted path, while its table may
+ * still name pages that are another request's by now.  A request with
+ * q_len[b] == 0 moves nothing.  A path with a node >= q_len[b], whose key and
+ * value were never written, sets SV_DEV_BAD_TREE, a negative q_len
+ * SV_DEV_BAD_LEN, and that request's cache is left as it is.  q_len NULL: as
+ * sv_kv_commit, where every request with accepted_len > 0 must be in the step.
  */
 SV_API sv_status sv_kv_commit(const sv_kv_cache* cache, int layers, int64_t layer_stride, int B,
                               const int32_t* block_table, int max_pages, const int32_t* kv_len,
                               const int32_t* accepted_nodes, int width,
                               const int32_t* accepted_len, int32_t* device_status, void* stream);
+SV_API sv_status sv_kv_commit_ragged(const sv_kv_cache* cache, int layers, int64_t layer_stride,
+                                     int B, const int32_t* block_table, int max_pages,
+                                     const int32_t* kv_len, const int32_t* q_len,
+                                     const int32_t* accepted_nodes, int width,
+                                     const int32_t* accepted_len, int32_t* device_status,
+                                     void* stream);
 
 /*
  * sv_set_knob -- process-wide test and tuning settings (not needed for

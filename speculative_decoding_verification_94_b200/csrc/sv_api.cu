@@ -1281,6 +1281,6 @@ const char* sv_status_string(sv_status s) {
   return "unknown status";
 }
 
-int sv_version(void) { return 300; }
+int sv_version(void) { return 310; }
 
 }  // extern "C"

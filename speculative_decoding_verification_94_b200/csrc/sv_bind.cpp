@@ -241,7 +241,7 @@ PyObject* do_attend(PyObject* const* a) {
 }
 
 PyObject* do_commit(PyObject* const* a) {
-  enum { kKc, kVc, kTable, kLen, kNodes, kAcc, kStatus };
+  enum { kKc, kVc, kTable, kLen, kNodes, kAcc, kQLen, kStatus };
   const Cache c = cache(a[kKc], a[kVc], true);
   if (c.layers == 0) return PyLong_FromLong(SV_OK);
   const at::Tensor& len = dense(a[kLen], "kv_len", at::kInt, c.dev);
@@ -250,9 +250,9 @@ PyObject* do_commit(PyObject* const* a) {
   int32_t* table = matrix(a[kTable], "block_table", c.dev, B, &max_pages);
   int32_t* nodes = matrix(a[kNodes], "accepted_nodes", c.dev, B, &width);
   const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.dev);
-  return PyLong_FromLong(sv_kv_commit(
+  return PyLong_FromLong(sv_kv_commit_ragged(
       &c.c, to_int(c.layers, "layers"), c.layer_stride, to_int(B, "B"), table, max_pages,
-      static_cast<int32_t*>(len.data_ptr()), nodes, width,
+      static_cast<int32_t*>(len.data_ptr()), ints(a[kQLen], "q_len", c.dev, B), nodes, width,
       ints(a[kAcc], "accepted_len", c.dev, B), ints(a[kStatus], "device_status", c.dev, 1),
       stream_of(c.dev)));
 }
@@ -280,7 +280,7 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef g_methods[] = {method<do_plan, 13>("plan"), method<do_append, 6>("append"),
-                           method<do_attend, 11>("attend"), method<do_commit, 7>("commit"),
+                           method<do_attend, 11>("attend"), method<do_commit, 8>("commit"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_svkv", nullptr, -1, g_methods};
 

@@ -464,6 +464,15 @@ sv_status sv_kv_commit(const sv_kv_cache* cache, int layers, int64_t layer_strid
                        const int32_t* block_table, int max_pages, const int32_t* kv_len,
                        const int32_t* accepted_nodes, int width, const int32_t* accepted_len,
                        int32_t* device_status, void* stream) {
+  return sv_kv_commit_ragged(cache, layers, layer_stride, B, block_table, max_pages, kv_len,
+                             nullptr, accepted_nodes, width, accepted_len, device_status, stream);
+}
+
+sv_status sv_kv_commit_ragged(const sv_kv_cache* cache, int layers, int64_t layer_stride, int B,
+                              const int32_t* block_table, int max_pages, const int32_t* kv_len,
+                              const int32_t* q_len, const int32_t* accepted_nodes, int width,
+                              const int32_t* accepted_len, int32_t* device_status,
+                              void* stream) {
   if (B < 0 || layers < 1 || layer_stride < 0 || max_pages < 1 || width < 1)
     return SV_ERR_INVALID_ARG;
   const sv_status st = check_cache(cache, layers, layer_stride);
@@ -472,7 +481,7 @@ sv_status sv_kv_commit(const sv_kv_cache* cache, int layers, int64_t layer_strid
   if (B == 0) return SV_OK;
   if (!block_table || !kv_len || !accepted_nodes || !accepted_len || !aligned(block_table, 4) ||
       !aligned(kv_len, 4) || !aligned(accepted_nodes, 4) || !aligned(accepted_len, 4) ||
-      !aligned_or_null(device_status, 4))
+      !aligned_or_null(q_len, 4) || !aligned_or_null(device_status, 4))
     return SV_ERR_INVALID_ARG;
   const int es = esize(cache->dtype);
   CommitParams p = {};
@@ -484,6 +493,7 @@ sv_status sv_kv_commit(const sv_kv_cache* cache, int layers, int64_t layer_strid
   p.c_head = cache->head_stride * es;
   p.table = block_table;
   p.kv_len = kv_len;
+  p.q_len = q_len;
   p.nodes = accepted_nodes;
   p.accepted = accepted_len;
   p.B = B;

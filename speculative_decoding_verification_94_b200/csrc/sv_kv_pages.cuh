@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
 struct CommitParams {
   unsigned char *kc, *vc;
   long long c_layer, c_page, c_token, c_head;  // bytes
-  const int32_t *table, *kv_len, *nodes, *accepted;
+  const int32_t *table, *kv_len, *q_len, *nodes, *accepted;
   int B, width, layers, heads, page, num_pages, max_pages;
   int head_chunks;
   FastDiv div_page, div_chunks, div_head;  // chunks: of a token; head: of a head
@@ -383,17 +383,20 @@ __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const CommitP
   const int32_t* row = p.table + (long long)b * p.max_pages;
   // the path's loads do not wait for one another
   const int a = p.accepted[b], base = p.kv_len[b];
+  const int wrote = p.q_len ? p.q_len[b] : 0x7fffffff;
   int nd = threadIdx.x < p.width ? nodes[threadIdx.x] : 0;
   int before = threadIdx.x > 0 && threadIdx.x < p.width ? nodes[threadIdx.x - 1] : -1;
-  if (a < 1) return;  // the root is in its place already; -1: failed verification
+  // The root is in its place already; -1: failed verification; a request that
+  // the step left out may have given its pages to another.
+  if (a < 1 || wrote == 0) return;
   int bad = 0;
-  if (a >= p.width || base < 0) {
+  if (a >= p.width || base < 0 || wrote < 0) {
     bad = SV_DEV_BAD_LEN;
   } else {
     for (int i = threadIdx.x; i <= a; i += kCommitThreads) {
       if (i >= kCommitThreads) nd = nodes[i], before = nodes[i - 1];
       const long long at[2] = {(long long)base + nd, (long long)base + i};
-      if (nd < i || (i == 0 && nd != 0) || before >= nd) {
+      if (nd < i || (i == 0 && nd != 0) || before >= nd || nd >= wrote) {
         bad |= SV_DEV_BAD_TREE;
         continue;
       }

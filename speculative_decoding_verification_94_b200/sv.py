@@ -42,7 +42,7 @@ EXPORTS = ("sv_verify_chain", "sv_verify_chain_ragged", "sv_verify_chain_noalloc
            "sv_verify_chain_workspace_size", "sv_verify_tree_workspace_size",
            "sv_extract_topk_workspace_size", "sv_kd_kl_loss_workspace_size",
            "sv_kv_plan", "sv_kv_append", "sv_kv_attend", "sv_kv_attend_scratch_size",
-           "sv_kv_commit",
+           "sv_kv_commit", "sv_kv_commit_ragged",
            "sv_device_status_check", "sv_status_string", "sv_version")
 
 
@@ -130,9 +130,11 @@ def lib() -> ctypes.CDLL:
             L.sv_kv_attend.argtypes = [vp, vp, i64, i64, ci, ci, ci, vp, ci, vp, vp, vp, cf, vp,
                                        vp, vp, sz, vp, vp]
             L.sv_kv_commit.argtypes = [vp, ci, i64, ci, vp, ci, vp, vp, ci, vp, vp, vp]
+            L.sv_kv_commit_ragged.argtypes = [vp, ci, i64, ci, vp, ci, vp, vp, vp, ci, vp, vp, vp]
             L.sv_kv_attend_scratch_size.argtypes = [ci, ci, ci, ci, ci, ci]
             L.sv_kv_attend_scratch_size.restype = sz
-            for f in ("sv_kv_plan", "sv_kv_append", "sv_kv_attend", "sv_kv_commit"):
+            for f in ("sv_kv_plan", "sv_kv_append", "sv_kv_attend", "sv_kv_commit",
+                      "sv_kv_commit_ragged"):
                 getattr(L, f).restype = ci
             L.sv_set_knob.argtypes = [ci, ctypes.c_longlong]
             L.sv_set_knob.restype = ci
@@ -636,10 +638,13 @@ def sv_kv_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
 
 def sv_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
                  kv_len: torch.Tensor, accepted_nodes: torch.Tensor, accepted_len: torch.Tensor,
-                 *, device_status: torch.Tensor | None = None, stream=None) -> None:
+                 *, q_len: torch.Tensor | None = None,
+                 device_status: torch.Tensor | None = None, stream=None) -> None:
     """Move accepted tree paths to the front of their step's tokens (see sv.h).
     Caches [num_pages, page_size, heads, head_dim] of one layer, or [layers,
     ...] of all of them; accepted_nodes [B, max_depth + 1] and accepted_len
-    [B] as sv_verify_tree_* return them."""
+    [B] as sv_verify_tree_* return them.  q_len [B]: the plan's (as
+    sv_kv_commit_ragged), without which every request with an accepted_len
+    above 0 must have been in the step with all its nodes."""
     _call("sv_kv_commit", _native().commit, stream, k_cache, v_cache, block_table, kv_len,
-          accepted_nodes, accepted_len, device_status)
+          accepted_nodes, accepted_len, q_len, device_status)

@@ -76,3 +76,46 @@ def test_attend_of_the_shortest_segments_repeats(n, hq, d):
     for _ in range(200):
         o = sv.sv_kv_attend(*args, q_len=i32(s["q_len"]), scale=s["scale"])
         assert torch.equal(o["out"], want[0]) and torch.equal(o["lse"], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_commit_moves_nothing_of_a_request_that_the_step_left_out(dtype):
+    """Request 0 ends and its pages go to request 1 in the same plan; the tree
+    call still finds it an accepted path."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    table, free = i32([[0, 1, -1], [2, -1, -1]]), i32([-1, -1, -1])
+    o = sv.sv_kv_plan(i32([6, 4]), table, i32([2, 1]), free, i32([0]), i32([0, 7]), 7, 4,
+                      written=i32([0, 0]), accepted_len=i32([0, 0]), release=i32([1, 0]))
+    assert table.tolist() == [[0, 1, -1], [2, 1, 0]] and o["q_len"].tolist() == [0, 7]
+    g = torch.Generator(device=DEV).manual_seed(0)
+    kc, vc = (torch.randn(2, 3, 4, 1, 8, generator=g, device=DEV).to(dt) for _ in range(2))
+    want = kc.clone(), vc.clone()
+    for w in want:  # request 1: position 5 (page 1) takes position 8 (page 0)
+        w[:, 1, 1] = w[:, 0, 0]
+    st = status()
+    sv.sv_kv_commit(kc, vc, table, o["kv_len"], i32([[0, 2], [0, 4]]), i32([1, 1]),
+                    q_len=o["q_len"], device_status=st)
+    assert int(st.item()) == 0
+    assert torch.equal(kc, want[0]) and torch.equal(vc, want[1])
+
+
+@pytest.mark.parametrize("q,bit", [([3, 6, 0], 0), ([2, 6, 0], sv.SV_DEV_BAD_TREE),
+                                   ([1, 6, 5], sv.SV_DEV_BAD_TREE),
+                                   ([-1, 6, 0], sv.SV_DEV_BAD_LEN), (None, 0)])
+def test_commit_moves_no_node_that_was_not_written(q, bit):
+    g = torch.Generator(device=DEV).manual_seed(1)
+    kc = torch.randn(8, 4, 2, 8, generator=g, device=DEV)
+    vc = torch.randn(8, 4, 2, 8, generator=g, device=DEV)
+    want = kc.clone(), vc.clone()
+    for w in want:
+        if q is None or q[0] == 3:
+            w[0, 1] = w[0, 2]           # request 0: node 2 to position 1
+        w[2, 2], w[2, 3] = w[2, 3].clone(), w[3, 2].clone()  # request 1: nodes 2, 5 behind 1 token
+        if q is None or q[2] == 5:
+            w[5, 1] = w[5, 3]           # request 2: node 3
+    st = status()
+    sv.sv_kv_commit(kc, vc, i32([[0, 1], [2, 3], [5, 6]]), i32([0, 1, 0]),
+                    i32([[0, 2, -1], [0, 2, 5], [0, 3, -1]]), i32([1, 2, 1]),
+                    q_len=None if q is None else i32(q), device_status=st)
+    assert int(st.item()) == bit
+    assert torch.equal(kc, want[0]) and torch.equal(vc, want[1])

@@ -1,0 +1,49 @@
+"""Promises of the paged cache calls that need no GPU: the header against the
+sources, refusals before any CUDA call, the oracle's view of idle requests."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv
+from speculative_decoding_verification_94_b200 import sv
+from tests.test_kv_abi import E, F, U, cache
+
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(),
+                            reason="fake-pointer validation tests run only without a GPU")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from speculative_decoding_verification_94_b200 import build
+    build.build()
+    return sv.lib()
+
+
+@no_gpu
+def test_commit_ragged_validates(lib):
+    def call(c=None, **kw):
+        a = dict(layers=2, ls=10 * 16 * 128, B=4, table=F, max_pages=8, kv_len=F, q_len=F, nodes=F,
+                 width=6, acc=F, status=None, stream=None)
+        a.update(kw)
+        return lib.sv_kv_commit_ragged(ctypes.byref(c or cache()), *a.values())
+    for kw in (dict(layers=0), dict(ls=-1), dict(ls=9 * 16 * 128), dict(B=-1), dict(table=None),
+               dict(kv_len=None), dict(nodes=None), dict(acc=None), dict(max_pages=0),
+               dict(width=0), dict(table=F + 2), dict(nodes=F + 2), dict(acc=F + 2),
+               dict(q_len=F + 2), dict(status=F + 2)):
+        assert call(**kw) == E, kw
+    assert call(cache(heads=0)) == E and call(width=1025) == U and call(B=65536) == U
+    assert call(B=0) == sv.SV_OK and call(B=0, q_len=None) == sv.SV_OK
+
+
+def test_a_request_left_out_may_name_another_requests_pages():
+    """Why a commit needs q_len: request 0 ends and gives back pages 0 and 1,
+    request 1 grows into them, and request 0's table still names them."""
+    o = kv.plan([6, 4], [0, 0], [0, 0], [1, 0], [0, 7], [[0, 1, -1], [2, -1, -1]], [2, 1],
+                [-1, -1, -1], 0, 4, 7)
+    assert o["q_len"].tolist() == [0, 7] and o["block_table"].tolist() == [[0, 1, -1], [2, 1, 0]]
+    cache4 = np.arange(3 * 4, dtype=np.float64).reshape(1, 3, 4, 1, 1)
+    # verification accepted a path for request 0 too
+    moved = kv.commit(cache4, o["block_table"], o["kv_len"], [[0, 2], [0, -1]], [1, 0])
+    assert not np.array_equal(moved, cache4)
