@@ -410,6 +410,7 @@ struct GenSmem {
   float v[kGenU][DP];
   float q[kGenR][DP];
   float p[kGenR][kGenU];
+  uint32_t seen[kGenR];  // in a tail: the keys that a row sees
   float alpha[kGenR], m[kGenR], l[kGenR];
   const unsigned char* row_k[kGenU];
   const unsigned char* row_v[kGenU];
@@ -541,6 +542,8 @@ __global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const Atten
             on = pos < cur.kv || (bits >> lane & 1u);
           }
           if (!on) x = -INFINITY;
+          const uint32_t bits = __ballot_sync(0xffffffffu, on);
+          if (lane == 0) sm.seen[r] = bits;
         }
         const float mn = fmaxf(m[j], warp_max(x));
         const float ms = mn == -INFINITY ? 0.f : mn;
@@ -579,16 +582,17 @@ __global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const Atten
           }
         }
       } else {
-        // keys that only some rows see: a weight of zero leaves the row as it
-        // is, whatever the key's value holds
+        // keys that only some rows see leave the others as they are, whatever
+        // their values hold
         for (int key = 0; key < kGenU; ++key)
 #pragma unroll
           for (int r = 0; r < kRows; ++r) {
             const float pr = sm.p[rg + r][key];
+            const bool on = sm.seen[rg + r] >> key & 1u;
 #pragma unroll
             for (int c = 0; c < kCols; ++c) {
               float& o = acc[r * kCols + c];
-              o = pr == 0.f ? o : fmaf(pr, sm.v[key][col + c * kGenThreads], o);
+              o = on ? fmaf(pr, sm.v[key][col + c * kGenThreads], o) : o;
             }
           }
       }

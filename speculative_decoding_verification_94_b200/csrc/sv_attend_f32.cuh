@@ -189,14 +189,16 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_f32_kernel(const Attend
       const int pos0 = t * kF32U + warp * kF32Keys;
       const bool tail = pos0 + kF32Keys > kv;
       float alpha[kRL];
+      uint32_t seen[kRL];  // in a tail: the keys that this lane's rows see
       bool grew = false;
 #pragma unroll
       for (int i = 0; i < kRL; ++i) {
         x[i] *= p.scale_log2;
+        seen[i] = 0;
         if (tail) {
           const int tok = min(fast_div(row0 + quarter * kRL + i, p.div_g), cur.q - 1);
-          const uint32_t bits = att_tail_bits<kF32Keys>(par, tok, pos0, kv, tree_ok);
-          if (!(bits >> key & 1u)) x[i] = -INFINITY;
+          seen[i] = att_tail_bits<kF32Keys>(par, tok, pos0, kv, tree_ok);
+          if (!(seen[i] >> key & 1u)) x[i] = -INFINITY;
         }
         float top = x[i];
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
@@ -244,12 +246,13 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_f32_kernel(const Attend
               acc[r][e] = f2_fma(p1, v1[e], acc[r][e]);
             }
           } else {
-            // keys that only some rows see: a weight of zero leaves the row as
-            // it is, whatever the key's value holds
+            // keys that only some rows see leave the others as they are,
+            // whatever their values hold
+            const uint32_t on = __shfl_sync(0xffffffffu, seen[r % kRL], r / kRL) >> 2 * a;
 #pragma unroll
             for (int e = 0; e < kV2; ++e) {
-              if (p0 != 0) acc[r][e] = f2_fma(p0, v0[e], acc[r][e]);
-              if (p1 != 0) acc[r][e] = f2_fma(p1, v1[e], acc[r][e]);
+              if (on & 1u) acc[r][e] = f2_fma(p0, v0[e], acc[r][e]);
+              if (on & 2u) acc[r][e] = f2_fma(p1, v1[e], acc[r][e]);
             }
           }
         }

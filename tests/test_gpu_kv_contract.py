@@ -119,3 +119,37 @@ def test_commit_moves_no_node_that_was_not_written(q, bit):
                     q_len=None if q is None else i32(q), device_status=st)
     assert int(st.item()) == bit
     assert torch.equal(kc, want[0]) and torch.equal(vc, want[1])
+
+
+@pytest.mark.parametrize("val", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("at", ["new", "committed"])
+@pytest.mark.parametrize("n,hq,d,dtype", [
+    (3, 4, 128, "f32"), (2, 8, 64, "f32"),                       # up to 8 rows
+    (6, 12, 64, "f32"), (6, 12, 128, "f32"),                     # more
+    (3, 4, 50, "f32"), (3, 4, 200, "f32"), (3, 4, 50, "bf16"),   # the general kernel
+    (3, 4, 128, "bf16"), (20, 8, 64, "bf16"), (20, 16, 128, "bf16")])
+def test_attend_values_that_are_not_finite_count_at_any_weight(n, hq, d, dtype, at, val):
+    """A key whose weight underflows to zero, its value not finite: the element
+    of the output is not finite for the rows that attend to it, and no other
+    element or row changes."""
+    s = scenario(2, n, hq, 2, d, 16, [5, 70], dtype, seed=23, q_scale=1.0)
+    s["q"][..., 0] = 30.0
+    for c in (s["kc"],):
+        c[..., 0] = 4.0
+    spots = []
+    for b in range(2):
+        pos = s["kv_len"][b] + 1 if at == "new" else s["kv_len"][b] - 1
+        spots.append((s["table"][b][pos // 16], pos % 16))
+        s["kc"][spots[-1]][:, 0] = -3000.0  # weight e^(-90000 / sqrt d) = 0
+    first = 1 if at == "new" else 0         # the first row that attends to it
+    clean, lse, st = call_attend(s)
+    assert st == 0 and torch.isfinite(clean.float()).all()
+    t = dict(s, vc=s["vc"].clone())
+    for x in spots:
+        t["vc"][x][:, 3] = val
+    out, lse2, st = call_attend(t)
+    assert st == 0 and torch.equal(lse, lse2)
+    keep = [c for c in range(d) if c != 3]
+    assert torch.equal(out[..., keep], clean[..., keep])
+    assert torch.equal(out[:, :first], clean[:, :first])
+    assert not torch.isfinite(out[:, first:, :, 3].float()).any()
