@@ -48,6 +48,13 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& h, uint32_t& l) {
   h = to_tf32(x);
   l = to_tf32(x - __uint_as_float(h));
 }
+// As split_tf32, for any finite x: what would round up past the largest number
+// is cut off, by at most 2^-11 of it there too.
+__device__ __forceinline__ void split_tf32_any(float x, uint32_t& h, uint32_t& l) {
+  h = to_tf32(x);
+  if (not_finite(__uint_as_float(h))) h = __float_as_uint(x) & 0xffffe000u;
+  l = to_tf32(x - __uint_as_float(h));
+}
 __device__ __forceinline__ void cut_tf32(float x, uint32_t& h, uint32_t& l) {
   h = __float_as_uint(x) & 0xffffe000u;
   l = to_tf32(x - __uint_as_float(h));
@@ -151,7 +158,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_tf32_kernel(const Atten
                                            (long long)(h * p.g + gi) * p.d + d];
       }
       uint32_t hi, lo;
-      split_tf32(x, hi, lo);
+      split_tf32_any(x, hi, lo);
       uint32_t* at = reinterpret_cast<uint32_t*>(s_q + r * C::kRowBytes +
                                                  (((d >> 2) ^ (r & 7)) << 4)) + (d & 3);
       at[0] = hi;

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from speculative_decoding_verification_94_b200 import sv
-from tests.test_gpu_kv import DEV, call_attend, i32, scenario, status
+from tests.test_gpu_kv import DEV, call_attend, check_attend, i32, scenario, status
 
 pytestmark = pytest.mark.gpu
 
@@ -153,3 +153,19 @@ def test_attend_values_that_are_not_finite_count_at_any_weight(n, hq, d, dtype, 
     assert torch.equal(out[..., keep], clean[..., keep])
     assert torch.equal(out[:, :first], clean[:, :first])
     assert not torch.isfinite(out[:, first:, :, 3].float()).any()
+
+
+@pytest.mark.parametrize("n,hq,d", [(2, 4, 64), (2, 4, 128), (6, 12, 64), (6, 12, 128), (3, 4, 50)])
+def test_attend_fp32_queries_up_to_the_largest_number(n, hq, d):
+    """q = +-FLT_MAX in one column, a scale that brings the scores back to a
+    few: the same finite result whatever the number of rows."""
+    s = scenario(2, n, hq, 2, d, 16, [5, 90], "f32", seed=29, q_scale=0.0)
+    big = torch.finfo(torch.float32).max
+    s["q"][..., 0] = big
+    s["q"][:, :, ::2, 0] = -big
+    s["kc"][..., 0] *= 0.2
+    s["kc"][..., 0].clamp_(-0.9, 0.9)
+    s["scale"] = 2.0 ** -126
+    out, lse, st = call_attend(s)
+    assert st == 0
+    check_attend(s, out, lse)
