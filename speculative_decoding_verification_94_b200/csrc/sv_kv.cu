@@ -54,9 +54,13 @@ sv_status check_cache(const sv_kv_cache* c, int layers = 1, long long layer_stri
   return SV_OK;
 }
 
+// Up to 48 KB of shared memory, the kernel's own (static) included, need no
+// permission; no kernel here has more than kStaticSmem of its own.
+constexpr int kStaticSmem = 16 * 1024;
+static_assert(2 * sizeof(long long) * kCommitMaxWidth <= kStaticSmem, "");
 template <class K, class Prm>
 cudaError_t launch(K kernel, const Prm& prm, dim3 grid, int threads, int smem, cudaStream_t s) {
-  cudaError_t e = smem > 48 * 1024
+  cudaError_t e = smem > 48 * 1024 - kStaticSmem
                       ? ensure_kernel_attrs(reinterpret_cast<const void*>(kernel), smem, false)
                       : cudaSuccess;
   if (e != cudaSuccess) return e;

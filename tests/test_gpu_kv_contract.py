@@ -1,6 +1,10 @@
 """What the header promises of the paged cache calls, beside the agreement with
 the oracle: precision of long contexts and of many rows, values that are not
 finite, requests that a step leaves out, bad page ids, limits of sizes."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -8,6 +12,7 @@ from speculative_decoding_verification_94_b200 import sv
 from tests.test_gpu_kv import DEV, call_attend, check_attend, i32, scenario, status
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def exact(s):
@@ -169,3 +174,24 @@ def test_attend_fp32_queries_up_to_the_largest_number(n, hq, d):
     out, lse, st = call_attend(s)
     assert st == 0
     check_attend(s, out, lse)
+
+
+FRESH_PLANS = """
+import random, sys, torch
+from oracle import kv as O
+from tests.test_gpu_kv import check_plan, run_plan
+from tests.test_kv_oracle import random_plan
+for B in (1, 2026, 2027, 2048, 2049):
+    args = random_plan(random.Random(B), B, 16, 12, 4, 900)
+    got, st = run_plan(args, 16, 4)
+    check_plan(got, O.plan(*args, 16, 4))
+print("plans ok")
+"""
+
+
+def test_plan_of_2048_requests_is_the_first_of_its_process():
+    """Batches whose shared memory passes 48 KB only with the kernel's own part,
+    before any larger batch has raised the kernel's limit."""
+    r = subprocess.run([sys.executable, "-c", FRESH_PLANS], cwd=ROOT, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "plans ok" in r.stdout, r.stderr[-2000:]
