@@ -436,7 +436,9 @@ typedef struct sv_kv_cache {
  *   A request with a length out of range (L_b + new_len[b] beyond max_pages
  *   pages, accepted_len[b] >= written[b] > 0, committed tokens without a page, ...)
  *   is left as it is, gets no new tokens and sets SV_DEV_BAD_LEN.  A page id
- *   outside [0, num_pages) sets SV_DEV_BAD_INDEX; its tokens' slots are -1.
+ *   outside [0, num_pages) sets SV_DEV_BAD_INDEX in the call that gives it
+ *   back (it is pushed as it is) and in the call that takes it from the stack
+ *   or maps a token to it; its tokens' slots are -1.
  *   No workspace.
  */
 SV_API sv_status sv_kv_plan(const int32_t* kv_len, const int32_t* written,

@@ -198,8 +198,9 @@ __global__ void __launch_bounds__(kPlanMaxThreads) kv_plan_kernel(const PlanPara
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = i0 + j * threads;
-        if (i < (int)give_all && (long long)count + i < p.num_pages)
-          p.free_pages[count + i] = id[j];
+        if (i >= (int)give_all) break;
+        if (id[j] < 0 || id[j] >= p.num_pages) kv_flag(p.status, SV_DEV_BAD_INDEX);
+        if ((long long)count + i < p.num_pages) p.free_pages[count + i] = id[j];
       }
     }
     __syncthreads();

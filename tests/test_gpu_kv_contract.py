@@ -8,8 +8,10 @@ import sys
 import pytest
 import torch
 
+from oracle import kv
 from speculative_decoding_verification_94_b200 import sv
-from tests.test_gpu_kv import DEV, call_attend, check_attend, i32, scenario, status
+from tests.test_gpu_kv import (DEV, call_attend, check_attend, check_plan, i32, run_plan, scenario,
+                               status)
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -195,3 +197,22 @@ def test_plan_of_2048_requests_is_the_first_of_its_process():
     r = subprocess.run([sys.executable, "-c", FRESH_PLANS], cwd=ROOT, capture_output=True,
                        text=True, timeout=300)
     assert r.returncode == 0 and "plans ok" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("bad", [-1, 9, 1 << 30])
+@pytest.mark.parametrize("release", [0, 1])
+def test_plan_reports_a_bad_page_in_the_call_that_gives_it_back(bad, release):
+    """Request 0 rolls back or ends; one of its pages is no page of the pool.
+    Request 1 keeps its page and nobody takes one."""
+    free = [7, 8] + [-9] * 7
+    rel = None if not release else [1, 0]
+    args = ([10, 4], [20, 0], [1, -1], rel, [0, 0], [[0, 1, bad, 3], [5, -7, -7, -7]], [2 + 2, 1],
+            free, 2)
+    got, st = run_plan(args, 8, 1)
+    check_plan(got, kv.plan(*args, 8, 1))
+    assert st == sv.SV_DEV_BAD_INDEX
+    assert bad in got["free_pages"][:int(got["free_count"][0])]
+    # the next plan, whose request takes it, says so again
+    after = (got["kv_len"].tolist(), None, None, None, [0, 27], got["block_table"].tolist(),
+             got["pages"].tolist(), got["free_pages"].tolist(), int(got["free_count"][0]))
+    assert run_plan(after, 8, 27)[1] == sv.SV_DEV_BAD_INDEX
