@@ -324,7 +324,7 @@ SV_API sv_status sv_verify_tree_sample(const void* target_logits, sv_dtype t_dty
  */
 SV_API sv_status sv_extract_topk_kd(const void* logits, sv_dtype dt, int rows, int V, int K,
                                     float temperature, float* topk_logp, int32_t* topk_idx,
-                                    float* lse, void* scratch, size_t scratch_bytes,
+                                    float* lse, void* workspace, size_t workspace_bytes,
                                     int32_t* device_status, void* stream);
 
 /*

@@ -1,6 +1,8 @@
 """Promises of the paged cache calls that need no GPU: the header against the
 sources, refusals before any CUDA call, the oracle's view of idle requests."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -10,6 +12,7 @@ from oracle import kv
 from speculative_decoding_verification_94_b200 import sv
 from tests.test_kv_abi import E, F, U, cache
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 no_gpu = pytest.mark.skipif(torch.cuda.is_available(),
                             reason="fake-pointer validation tests run only without a GPU")
 
@@ -47,3 +50,28 @@ def test_a_request_left_out_may_name_another_requests_pages():
     # verification accepted a path for request 0 too
     moved = kv.commit(cache4, o["block_table"], o["kv_len"], [[0, 2], [0, -1]], [1, 0])
     assert not np.array_equal(moved, cache4)
+
+
+def _parameters(text, name, end):
+    """Parameter names of a function's declaration (end ";") or definition ("{") in C."""
+    m = re.search(r"\b%s\s*\(([^()]*(?:\([^()]*\)[^()]*)*)\)\s*%s" % (name, end), text)
+    if not m or m.group(1).strip() in ("", "void"):
+        return [] if m else None
+    return [re.findall(r"\w+", re.sub(r"\[.*?\]", "", p))[-1] for p in m.group(1).split(",")]
+
+
+def test_the_header_names_its_parameters_as_the_sources_do():
+    """A caller reads the prototype: its names are the documented contract
+    (a workspace is zeroed, scratch may hold anything)."""
+    def plain(path):
+        text = re.sub(r"/\*.*?\*/", "", open(path).read(), flags=re.S)
+        return re.sub(r"//[^\n]*", "", text)
+    header = plain(os.path.join(ROOT, "include", "sv.h"))
+    src = os.path.join(ROOT, "speculative_decoding_verification_94_b200", "csrc")
+    api = plain(os.path.join(src, "sv_api.cu")), plain(os.path.join(src, "sv_kv.cu"))
+    api = "\n".join(t[t.index('extern "C"'):] for t in api)
+    short = {"knob_id": "knob", "w": "device_status_word"}  # where the source needs the name itself
+    for name in sv.EXPORTS:
+        declared, defined = _parameters(header, name, ";"), _parameters(api, name, "{")
+        assert declared is not None and defined is not None, name
+        assert declared == [short.get(p, p) for p in defined], name
