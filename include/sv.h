@@ -421,6 +421,10 @@ typedef struct sv_kv_cache {
  *   (q_len[b] = 0, SV_DEV_NO_PAGES); their commit stands.
  *   slot_map[b, i] = block_table[b, t / page_size] * page_size + t % page_size
  *   with t = L_b + i for i < q_len[b], else -1; positions[b, i] = t, else -1.
+ *   positions are places in the cache.  In a prompt or a chain they are also the
+ *   tokens' positions in the text (what a rotary embedding takes); in a tree
+ *   node i stands at L_b + depth(i) in the text, depth(i) being the number of
+ *   its ancestors, which is also its place in the cache once it is committed.
  *
  * Arguments
  *   kv_len [B]; written, accepted_len, release [B] or NULL; new_len [B] in
@@ -477,7 +481,8 @@ SV_API sv_status sv_kv_append(const sv_kv_cache* cache, const void* k, const voi
  *   lse[b, i, x] = log sum_j exp(scale * q[b, i, x] . k_j).
  *   A key that a row does not attend to never affects it, whatever the cache
  *   holds there.  A value that it does attend to and that is not finite makes
- *   that element of the output not finite; q and the attended keys are finite.  Tokens i >= q_len[b] give zeros and lse -inf.
+ *   that element of the output not finite; q and the attended keys are finite.
+ *   Tokens i >= q_len[b] give zeros and lse -inf.
  *
  * Arguments
  *   q [B, n, q_heads, head_dim] of the cache's type, the heads of a token

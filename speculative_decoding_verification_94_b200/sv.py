@@ -598,7 +598,9 @@ def sv_kv_plan(kv_len: torch.Tensor, block_table: torch.Tensor, pages: torch.Ten
     """Commit the last step, give back and take pages, and map the new tokens
     to slots (see sv.h).  block_table [B, max_pages] and free_pages change in
     place.  Returns kv_len, pages, free_count, q_len, slot_map and positions
-    (allocated unless given in `out`, where the first four may be inputs)."""
+    (allocated unless given in `out`, where the first four may be inputs).
+    positions are places in the cache; a tree's node stands at kv_len + its
+    depth in the text."""
     return _call("sv_kv_plan", _native().plan, stream, kv_len, block_table, pages, free_pages,
                  free_count, new_len, max_new, page_size, written, accepted_len, release, out,
                  device_status)

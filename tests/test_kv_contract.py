@@ -75,3 +75,30 @@ def test_the_header_names_its_parameters_as_the_sources_do():
         declared, defined = _parameters(header, name, ";"), _parameters(api, name, "{")
         assert declared is not None and defined is not None, name
         assert declared == [short.get(p, p) for p in defined], name
+
+
+def test_readme_text_positions_of_a_tree_are_places_after_the_commit():
+    """The README's lines for the depths of a tree, run on random trees: the
+    i-th node of every path from the root stands at kv_len + i, which is where
+    a commit of that path puts it, while the plan's positions do not."""
+    text = open(os.path.join(ROOT, "README.md")).read()
+    block = text[text.index("depth = torch.zeros_like(parents)"):]
+    block = block[:block.index("att = ")]
+    rng = np.random.default_rng(0)
+    n = 24
+    par = [[-1] + [int(rng.integers(0, j)) for j in range(1, n)] for _ in range(6)]
+    scope = dict(torch=torch, parents=torch.tensor(par, dtype=torch.int32),
+                 plan=dict(kv_len=torch.tensor([0, 3, 50, 7, 1, 2], dtype=torch.int32)))
+    exec(block, scope)
+    got = scope["text_positions"]
+    for b, p in enumerate(par):
+        base = int(scope["plan"]["kv_len"][b])
+        for j in range(n):
+            path = kv.ancestors(p, j)[::-1]
+            assert got[b, path].tolist() == [base + i for i in range(len(path))]
+            # a commit of this path moves node path[i] from place path[i] to place i
+            keep = np.arange(base + n, dtype=np.float64).reshape(1, base + n, 1, 1, 1)
+            table = [list(range(base + n))]
+            moved = kv.commit(keep, table, [base], [path], [len(path) - 1])
+            assert [int(moved[0, int(got[b, x]), 0, 0, 0]) - base for x in path] == path
+    assert not torch.equal(got, scope["plan"]["kv_len"][:, None] + torch.arange(n))
