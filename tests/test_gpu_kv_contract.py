@@ -216,3 +216,55 @@ def test_plan_reports_a_bad_page_in_the_call_that_gives_it_back(bad, release):
     after = (got["kv_len"].tolist(), None, None, None, [0, 27], got["block_table"].tolist(),
              got["pages"].tolist(), got["free_pages"].tolist(), int(got["free_count"][0]))
     assert run_plan(after, 8, 27)[1] == sv.SV_DEV_BAD_INDEX
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,hq,d", [(1, 4, 64), (20, 4, 64), (1, 5, 128), (5, 8, 128), (16, 8, 128)])
+@pytest.mark.parametrize("keys", [31007, 130001, 719999])
+def test_attend_long_contexts(keys, n, hq, d, dtype):
+    """One request over nearly all blocks and a short one beside it.  Values of
+    one sign that grow along the context, so that the output is of the size of
+    sum p |v|: a lost or doubled part of a sequence (a 300th at least) moves lse
+    by 3e-3, and parts in another order, or of another page, the output.
+
+    bf16: rounding the exact output errs by 1.2e-3 to 1.7e-3 of its size, weights
+    by 2^-16, and sums by a warp's run of at most 200 steps and the 300 parts
+    joined, 500 2^-24 = 3e-5 in all: 5 % more than the rounding alone are allowed.
+    fp32: the same 3e-5, and twice the score's error below.
+    lse: 500 half steps, and (d + 4) + 20 half steps of a score's largest sum of
+    |q k| (20 for products in two parts)."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    page, num = 16, -(-(keys + n) // 16)
+    g = torch.Generator(device=DEV).manual_seed(keys + n)
+    k = torch.randn(num + 4, page, 1, d, generator=g, device=DEV).to(dt)
+    v = torch.rand(num + 4, page, 1, d, generator=g, device=DEV)
+    order = torch.randperm(num, generator=g, device=DEV)
+    where = torch.empty(num, device=DEV)
+    where[order] = torch.arange(num, device=DEV) / num
+    v[:num] += 2 * where[:, None, None, None]  # page j of the context: + 2 j / num
+    v = v.to(dt)
+    q = torch.randn(2, n, hq, d, generator=g, device=DEV).to(dt)
+    table = torch.full((2, num), -1, dtype=torch.int32, device=DEV)
+    table[0] = order.int()
+    table[1, :3] = torch.tensor([num, num + 2, num + 1], dtype=torch.int32)
+    lens = [keys, 17]
+    st = status()
+    o = sv.sv_kv_attend(q, k, v, table, i32(lens), device_status=st)
+    assert int(st.item()) == 0
+    eps = 2.0 ** -24
+    for b in range(2):
+        ids = table[b, :-(-(lens[b] + n) // page)].long()
+        kk, vv = (x[ids].reshape(-1, d)[:lens[b] + n].double() for x in (k, v))
+        qq = q[b].double().view(n * hq, d)
+        z = qq @ kk.T * d ** -0.5
+        size = float((qq.abs() @ kk.abs().T).amax()) * d ** -0.5
+        see = lens[b] + torch.arange(n, device=DEV).repeat_interleave(hq)
+        z[torch.arange(lens[b] + n, device=DEV)[None, :] > see[:, None]] = float("-inf")
+        ref = torch.softmax(z, -1) @ vv
+        err = float((o["out"][b].double().view(-1, d) - ref).norm() / ref.norm())
+        score = (d + 24) * size * eps
+        least = float((ref.to(dt).double() - ref).norm() / ref.norm())
+        limit = 1.05 * least if dtype == "bf16" else least + 500 * eps + 2 * score
+        assert limit < 2e-3 and err <= limit, (b, err, limit)
+        off = (o["lse"][b].double().view(-1) - torch.logsumexp(z, -1)).abs().max()
+        assert float(off) <= 500 * eps + score + 4 * eps * 20
