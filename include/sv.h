@@ -530,7 +530,8 @@ SV_API sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t b
  *   A path that does not ascend from 0 sets SV_DEV_BAD_TREE, a position
  *   outside the table or accepted_len >= width SV_DEV_BAD_LEN, a bad page
  *   SV_DEV_BAD_INDEX; such a request's cache is left as it is.
- *   0 <= B <= 65535.  No workspace.
+ *   0 <= B <= 65535, a token's row below 2^30 pieces of the widest access its
+ *   alignment allows (sv_kv_append too), 2 * layers of them as well.  No workspace.
  *
  * sv_kv_commit_ragged -- the same for a step that not every request took part
  * in with all n nodes: q_len [B] as sv_kv_plan gives it.  The tree calls

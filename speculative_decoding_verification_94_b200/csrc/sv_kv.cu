@@ -343,6 +343,7 @@ sv_status sv_kv_append(const sv_kv_cache* cache, const void* k, const void* v, i
   const long long row = (long long)cache->head_dim * es;
   const int w = common_width({addr(k), addr(v), addr(cache->k), addr(cache->v), p.in_b, p.in_t,
                               p.c_page, p.c_token, p.c_head, row});
+  if (row / w * p.heads > 0x3fffffffLL) return SV_ERR_UNSUPPORTED;  // counted in int
   p.head_chunks = (int)(row / w);
   if (p.heads > 1 && p.c_head == row) {  // a token's heads are one row
     p.head_chunks *= p.heads;
@@ -511,13 +512,16 @@ sv_status sv_kv_commit_ragged(const sv_kv_cache* cache, int layers, int64_t laye
   const long long row = (long long)cache->head_dim * es;
   const int w = common_width(
       {addr(cache->k), addr(cache->v), p.c_layer, p.c_page, p.c_token, p.c_head, row});
+  const long long per_token = row / w * p.heads;
+  if (per_token > 0x3fffffffLL || 2LL * layers * per_token > 0x3fffffffLL ||  // counted in int
+      cache->page_size > (1 << 30))
+    return SV_ERR_UNSUPPORTED;
+  const long long items = 2LL * layers * per_token;
   p.head_chunks = (int)(row / w);
   if (p.heads > 1 && p.c_head == row) {  // a token's heads are one row
     p.head_chunks *= p.heads;
     p.heads = 1;
   }
-  const long long items = 2LL * layers * p.heads * p.head_chunks;
-  if (items > 0x3fffffffLL || cache->page_size > (1 << 30)) return SV_ERR_UNSUPPORTED;
   p.div_page = make_fastdiv(cache->page_size);
   p.div_chunks = make_fastdiv(p.heads * p.head_chunks);
   p.div_head = make_fastdiv(p.head_chunks);

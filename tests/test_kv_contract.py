@@ -102,3 +102,22 @@ def test_readme_text_positions_of_a_tree_are_places_after_the_commit():
             moved = kv.commit(keep, table, [base], [path], [len(path) - 1])
             assert [int(moved[0, int(got[b, x]), 0, 0, 0]) - base for x in path] == path
     assert not torch.equal(got, scope["plan"]["kv_len"][:, None] + torch.arange(n))
+
+
+@no_gpu
+def test_tokens_of_more_pieces_than_an_int_counts_are_refused(lib):
+    """16-byte to 2-byte pieces of a token, 2^29 to 2^32 of them: refused
+    before a count in int can wrap."""
+    for heads, d, gap, off in ((1 << 30, 8, 0, 0), (1 << 28, 64, 0, 0), (1 << 26, 128, 0, 0),
+                               (1 << 27, 32, 0, 2), (1 << 27, 32, 8, 0), (1 << 27, 33, 0, 0)):
+        big = cache(heads=heads, head_dim=d, head_stride=d + gap, token_stride=heads * (d + gap),
+                    page_stride=16 * heads * (d + gap), k=F + off, v=F + off)
+        ts = heads * d
+        pieces = heads * d * 2 // (2 if off or d % 2 else 16)
+        got = lib.sv_kv_append(ctypes.byref(big), F, F, 4, 3, 3 * ts, ts, F, None, None)
+        assert (got == U) == (pieces > 0x3fffffff), (heads, d)
+        got = lib.sv_kv_commit(ctypes.byref(big), 2, 10 * 16 * heads * (d + gap), 4, F, 8, F, F, 6,
+                               F, None, None)
+        assert (got == U) == (4 * pieces > 0x3fffffff), (heads, d)
+    assert lib.sv_kv_commit(ctypes.byref(cache()), 0x7fffffff, 10 * 16 * 128, 4, F, 8, F, F, 6, F,
+                            None, None) == U
