@@ -78,6 +78,15 @@ int to_int(PyObject* o, const char* name) {
   return to_int((int64_t)x, name);
 }
 
+// The stride of a dimension that has one: with a single entry it is never
+// taken, and torch lets it hold anything.
+int64_t step(const at::Tensor& t, int64_t dim) { return t.size(dim) > 1 ? t.stride(dim) : 0; }
+bool same_steps(const at::Tensor& a, const at::Tensor& b) {
+  for (int64_t i = 0; i < a.dim(); ++i)
+    if (step(a, i) != step(b, i)) return false;
+  return true;
+}
+
 // Caches [num_pages, page_size, heads, head_dim], or [layers, ...] of them.
 struct Cache {
   sv_kv_cache c;
@@ -92,7 +101,7 @@ Cache cache(PyObject* ko, PyObject* vo, bool layered) {
       k.get_device() != v.get_device() || !(n == 4 || (layered && n == 5)))
     value_error("k_cache and v_cache must be [num_pages, page_size, heads, head_dim] of one "
                 "shape, type and device");
-  if (k.strides() != v.strides() || (k.stride(n - 1) != 1 && k.size(n - 1) > 1))
+  if (!same_steps(k, v) || (k.size(n - 1) > 1 && k.stride(n - 1) != 1))
     value_error("k_cache and v_cache must have the same strides and dense rows");
   Cache r = {};
   r.type = k.scalar_type();
@@ -100,7 +109,7 @@ Cache cache(PyObject* ko, PyObject* vo, bool layered) {
     type_error(std::string("unsupported dtype ") + c10::toString(r.type));
   r.dev = k.get_device();
   r.layers = n == 5 ? k.size(0) : 1;
-  r.layer_stride = n == 5 ? k.stride(0) : 0;
+  r.layer_stride = n == 5 ? step(k, 0) : 0;
   r.c.k = k.data_ptr();
   r.c.v = v.data_ptr();
   r.c.dtype = r.type == at::kBFloat16 ? SV_BF16 : SV_F32;
@@ -108,9 +117,9 @@ Cache cache(PyObject* ko, PyObject* vo, bool layered) {
   r.c.page_size = to_int(k.size(n - 3), "page_size");
   r.c.heads = to_int(k.size(n - 2), "heads");
   r.c.head_dim = to_int(k.size(n - 1), "head_dim");
-  r.c.page_stride = k.stride(n - 4);
-  r.c.token_stride = k.stride(n - 3);
-  r.c.head_stride = k.stride(n - 2);
+  r.c.page_stride = step(k, n - 4);
+  r.c.token_stride = step(k, n - 3);
+  r.c.head_stride = step(k, n - 2);
   return r;
 }
 
@@ -195,12 +204,12 @@ PyObject* do_append(PyObject* const* a) {
   const Cache c = cache(a[kKc], a[kVc], false);
   const at::Tensor& k = token_rows(a[kK], "k", c, c.c.heads);
   const at::Tensor& v = token_rows(a[kV], "v", c, c.c.heads);
-  if (k.sizes() != v.sizes() || k.strides() != v.strides())
+  if (k.sizes() != v.sizes() || !same_steps(k, v))
     value_error("k and v must have the same shape and strides");
   const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.dev);
   return PyLong_FromLong(
       sv_kv_append(&c.c, k.data_ptr(), v.data_ptr(), to_int(k.size(0), "B"), to_int(k.size(1), "n"),
-                   k.stride(0), k.stride(1),
+                   step(k, 0), step(k, 1),
                    data<int64_t>(a[kSlots], "slot_map", at::kLong, c.dev, k.size(0) * k.size(1)),
                    ints(a[kStatus], "device_status", c.dev, 1), stream_of(c.dev)));
 }
@@ -232,7 +241,7 @@ PyObject* do_attend(PyObject* const* a) {
   else
     own = dense(a[kScratch], "scratch", at::kByte, c.dev);
   const sv_status st = sv_kv_attend(
-      &c.c, q.data_ptr(), q.stride(0), q.stride(1), to_int(B, "B"), to_int(n, "n"),
+      &c.c, q.data_ptr(), step(q, 0), step(q, 1), to_int(B, "B"), to_int(n, "n"),
       to_int(hq, "q_heads"), table, max_pages, ints(a[kLen], "kv_len", c.dev, B),
       ints(a[kQLen], "q_len", c.dev, B), ints(a[kParents], "parents", c.dev, B * n), (float)scale,
       out, lse, own.data_ptr(), (size_t)own.numel(), ints(a[kStatus], "device_status", c.dev, 1),

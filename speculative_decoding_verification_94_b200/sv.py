@@ -609,9 +609,10 @@ def sv_kv_plan(kv_len: torch.Tensor, block_table: torch.Tensor, pages: torch.Ten
 def sv_kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cache: torch.Tensor,
                  v_cache: torch.Tensor, *, device_status: torch.Tensor | None = None,
                  stream=None) -> None:
-    """Write new tokens' keys and values [B, n, heads, head_dim] to their
-    slots (slot_map [B, n] int64, negative: none) of the caches [num_pages,
-    page_size, heads, head_dim] (see sv.h)."""
+    """Write new tokens' keys and values [B, n, heads, head_dim] (of the same
+    strides, each token's heads dense) to their slots (slot_map [B, n] int64,
+    negative: none) of the caches [num_pages, page_size, heads, head_dim] (see
+    sv.h)."""
     _call("sv_kv_append", _native().append, stream, k, v, slot_map, k_cache, v_cache,
           device_status)
 

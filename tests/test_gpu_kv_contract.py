@@ -268,3 +268,46 @@ def test_attend_long_contexts(keys, n, hq, d, dtype):
         assert limit < 2e-3 and err <= limit, (b, err, limit)
         off = (o["lse"][b].double().view(-1) - torch.logsumexp(z, -1)).abs().max()
         assert float(off) <= 500 * eps + score + 4 * eps * 20
+
+
+@pytest.mark.parametrize("B,n", [(1, 3), (4, 1), (1, 1)])
+def test_append_takes_any_stride_of_a_single_request_or_token(B, n):
+    """k out of a rotary embedding (dense), v still a part of the projection:
+    where they differ, there is one request or one token."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    fused = torch.randn(B, n, 6, 64, generator=g, device=DEV)
+    v = fused[:, :, 4:]
+    k = torch.randn(B * n * 2 * 64 * 9, generator=g, device=DEV)
+    # k with v's strides where there is a choice to be taken, odd ones elsewhere
+    k = k.as_strided((B, n, 2, 64), (v.stride(0) if B > 1 else 7, v.stride(1) if n > 1 else 11, 64, 1))
+    kc, vc = torch.zeros(6, 4, 2, 64, device=DEV), torch.zeros(6, 4, 2, 64, device=DEV)
+    slots = torch.arange(B * n, device=DEV).view(B, n) * 2 + 1
+    sv.sv_kv_append(k, v, slots, kc, vc)
+    for c, x in ((kc, k), (vc, v)):
+        want = torch.zeros(24, 2, 64, device=DEV)
+        want[slots.view(-1)] = x.reshape(-1, 2, 64)
+        assert torch.equal(c.view(24, 2, 64), want)
+
+
+@pytest.mark.parametrize("n,hq,dtype", [(1, 4, "bf16"), (6, 8, "bf16"), (1, 4, "f32"),
+                                        (6, 8, "f32")])
+def test_attend_strides_that_are_never_taken_change_nothing(n, hq, dtype):
+    """One request, one page and one key head with odd strides of their own:
+    the same kernel, so the same bits."""
+    s = scenario(1, n, hq, 1, 64, 128, [100], dtype, seed=37, spare=0)
+    want = call_attend(s)
+    assert s["kc"].shape[0] == 1 and want[2] == 0
+    odd = dict(s)
+    odd["q"] = s["q"].as_strided(s["q"].shape, (12345,) + s["q"].stride()[1:])
+    for name, page in (("kc", 3), ("vc", 5)):
+        c = s[name]
+        odd[name] = c.as_strided(c.shape, (page, c.stride(1), 2 * page + 1, 1))
+    out, lse, st = call_attend(odd)
+    assert st == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    st, old = status(), (s["kc"].clone(), s["vc"].clone())
+    sv.sv_kv_commit(odd["kc"], odd["vc"], i32(s["table"]), i32([3]), i32([[0, 2, 5]]), i32([2]),
+                    device_status=st)
+    assert int(st.item()) == 0
+    for c, was in zip((s["kc"], s["vc"]), old):
+        was[0, 4], was[0, 5] = was[0, 5].clone(), was[0, 8].clone()
+        assert torch.equal(c, was)
