@@ -5,6 +5,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from importlib import metadata
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -12,13 +13,21 @@ CSRC = PKG / "csrc"
 SOURCES = ["sv_api.cu", "sv_chain_bf16.cu", "sv_chain_f32.cu", "sv_kv.cu"]
 LIB = PKG / "libsv.so"
 BIND = PKG / "_svkv.so"  # Python module over libsv.so, for the paged cache calls
+BOUND = PKG / "_build" / "_svkv.txt"  # the torch and Python it was built for
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-fvisibility=hidden"]
 
 
+def _bound_to() -> str:
+    """What the native half of the binding is compiled against."""
+    return f"torch {metadata.version('torch')}, {sys.implementation.cache_tag}"
+
+
 def _stale() -> bool:
     if not LIB.exists() or not BIND.exists():
+        return True
+    if not BOUND.exists() or BOUND.read_text() != _bound_to():
         return True
     t = min(LIB.stat().st_mtime, BIND.stat().st_mtime)
     deps = list(CSRC.glob("*")) + [PKG.parent / "include" / "sv.h", Path(__file__)]
@@ -74,6 +83,7 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 4) -> Path:
     subprocess.run([os.environ.get("CXX", "g++"), "-shared", str(objdir / "sv_bind.o"), "-o",
                     str(tmp_bind), f"-L{PKG}", "-l:libsv.so", "-Wl,-rpath,$ORIGIN", *libs, "-lc10",
                     "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], check=True)
+    BOUND.write_text(_bound_to())
     os.replace(tmp_bind, BIND)
     return LIB
 

@@ -121,3 +121,13 @@ def test_tokens_of_more_pieces_than_an_int_counts_are_refused(lib):
         assert (got == U) == (4 * pieces > 0x3fffffff), (heads, d)
     assert lib.sv_kv_commit(ctypes.byref(cache()), 0x7fffffff, 10 * 16 * 128, 4, F, 8, F, F, 6, F,
                             None, None) == U
+
+
+def test_the_binding_is_rebuilt_for_another_torch(lib, monkeypatch):
+    from importlib import metadata
+
+    from speculative_decoding_verification_94_b200 import build
+    assert not build._stale()
+    version = metadata.version
+    monkeypatch.setattr(metadata, "version", lambda name: version(name) + ".other")
+    assert build._stale()
