@@ -16,17 +16,19 @@
 // bf16).  128 rows take two products for it (16 instructions a tile instead of
 // 8).  Repeated rows take none: copies c and c ^ 1 of a row are partners that
 // share a maximum, and the rests of one's part go to the other's lanes, which
-// had zeros there.  The partner computes those weights from its own lanes of S.
+// had zeros there.  The partner computes those weights from its own lanes of S
+// (two copies tell each other their maxima, of four each looks at both parts).
 //
 // Bound.  One SM's share of HBM brings the 64 KB of a tile in 1.5 us.  An
 // instruction of the products (16 of the summed index) took 95 cycles whether
 // it was 64 or 128 wide, so a tile's 16 take 0.8 us (24 with 128 rows: 1.2 us),
 // and a softmax of 128 rows 0.9 us without the rests.  With the products and the
 // softmax taken out, the copies alone needed 109 us for 130,000 keys of 8 heads
-// (40 rows).  What the rests cost, from L2: nothing with 28 rows (32 requests of
-// 700 to 9000 keys, 68 us), 96 -> 101 us with 40 (130,000 keys), 50 -> 61 us
+// (40 rows).  What the rests cost: 69.7 -> 70.6 us with 28 rows (32 requests of
+// 700 to 9000 keys), 105.7 -> 112.3 us with 40 (130,000 keys), 49.4 -> 61.5 us
 // with 256 (8 requests of 2000 to 8000 keys; 9 us of it in the softmax, 3 in the
-// products).  What was slower: S in halves of 64 keys (32 instructions a tile).
+// products).  In second products for all numbers of rows: 74, 117 and 61.5 us.
+// What was slower too: S in halves of 64 keys (32 instructions a tile).
 //
 // Roles.  Two warps issue the copies (keys, values), one the products, as
 // their operands arrive, one fills the rows behind a request's own.  Two warp
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t *k_full = bars, *k_empty = bars + 3, *v_full = bars + 6, *v_empty = bars + 9,
            *s_full = bars + 12, *p_ready = bars + 14, *pv_done = bars + 16, *q_full = bars + 18,
-           *q_first = bars + 19;
+           *q_first = bars + 19, *tops = bars + 20;  // tops: RT 64 only
   int* misc = reinterpret_cast<int*>(smem + C::kOffMisc);
   volatile int* s_abort = misc;      // a wait ran out
   int* s_bad = misc + 1;             // the segment's keys are on a bad page
@@ -271,6 +273,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(s_full + i, 1);
       mbar_init(p_ready + i, 128);
       mbar_init(pv_done + i, 1);
+      mbar_init(tops + i, 128);
     }
     mbar_init(q_full, kTcSoftmax);
     mbar_init(q_first, kTcSoftmax);
@@ -513,6 +516,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // The chunks of this copy, then those of its partner, whose weights'
         // rests go to this copy's lanes.
         constexpr int kOwn = kKeys / 32, kChunks = kCopies > 1 ? 2 * kOwn : kOwn;
+        constexpr int kSeen = kCopies == 2 ? kOwn : kChunks;  // looked at for the maximum
         auto chunk = [&](int c) { return c < kOwn ? copy * kOwn + c : (copy ^ 1) * kOwn + c - kOwn; };
         const bool tail = (tile0 + k + 1) * kTcU > kv;
         auto seen = [&](int c) {  // which of chunk c's keys this row sees
@@ -532,9 +536,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         float top = -INFINITY;
         tc_ld(s_at + chunk(0) * 32, x[0]);
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
+        for (int c = 0; c < kSeen; ++c) {
           tc_wait_ld(x[c & 1]);
-          if (c + 1 < kChunks) tc_ld(s_at + chunk(c + 1) * 32, x[(c + 1) & 1]);
+          if (c + 1 < kSeen) tc_ld(s_at + chunk(c + 1) * 32, x[(c + 1) & 1]);
           hide(c, x[c & 1]);
           float t2[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -543,7 +547,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     __uint_as_float(x[c & 1][e + 1]));
           top = fmaxf(fmaxf(t2[0], t2[1]), fmaxf(t2[2], t2[3]));
         }
-        if (kChunks > 2) tc_ld(s_at + chunk(0) * 32, x[0]);  // two are still there
+        if (kSeen > 2) tc_ld(s_at + chunk(0) * 32, x[0]);  // two are still there
+        if constexpr (kSeen < kChunks) {
+          // the partner's maximum, from shared memory; a place is written again
+          // two tiles on, when everyone has passed the next one's barrier
+          float* both = reinterpret_cast<float*>(s_ml + w * 128) + (tiles_done & 1);
+          both[2 * lr] = top;
+          mbar_arrive(tops + w);
+          dead = !__all_sync(0xffffffffu, tc_wait(tops + w, tiles_done & 1, wait_ns));
+          if (dead) {
+            *s_abort = 1;
+            break;
+          }
+          top = fmaxf(top, both[2 * (lr ^ RT)]);
+        }
         top *= p.scale_log2;  // scale > 0 here
         // a new maximum only when weights would pass 2^8
         const bool grow = top > m + 8.f || (m == -INFINITY && top != -INFINITY);
@@ -576,9 +593,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // rests in the second half, or in the partner's lanes
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          if (kChunks > 2) {
+          if (kSeen > 2) {
             tc_wait_ld(x[c & 1]);
             if (c + 1 < kChunks) tc_ld(s_at + chunk(c + 1) * 32, x[(c + 1) & 1]);
+            hide(c, x[c & 1]);
+          } else if (c >= kSeen) {
+            tc_wait_ld(x[c & 1]);
             hide(c, x[c & 1]);
           }
           uint32_t y[16], rest[16];
@@ -593,11 +613,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             b = pow2(b);
             if (c < kOwn) sum[e & 1] = f2_add(sum[e & 1], f2_pack(a, b));
             y[e] = pack_bf16(a, b);
-            if (kCopies == 1 || c >= kOwn)
-              rest[e] = pack_bf16(a - bf16_lo(y[e]), b - bf16_hi(y[e]));
+            if (kCopies == 1 || c >= kOwn) {
+              float ra, rb;
+              f2_unpack(f2_fma(f2_pack(bf16_lo(y[e]), bf16_hi(y[e])), f2_pack(-1.f, -1.f),
+                               f2_pack(a, b)),
+                        ra, rb);
+              rest[e] = pack_bf16(ra, rb);
+            }
           }
           tc_st(s_at + chunk(c) * 32, c < kOwn ? y : rest);
           if (kCopies == 1) tc_st(s_at + chunk(c) * 32 + 16, rest);
+          if (kSeen == 2 && c + 2 < kChunks) tc_ld(s_at + chunk(c + 2) * 32, x[c & 1]);
         }
         if constexpr (kCopies > 2) {  // the other copies' keys
           const uint32_t zero[16] = {};
