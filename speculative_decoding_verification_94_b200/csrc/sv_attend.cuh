@@ -236,6 +236,11 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+// In a tile that only some rows see all of, a weight of +0 says that the row
+// does not attend to the key; one that has underflowed becomes -0.
+__device__ __forceinline__ float att_mark_seen(float w, bool off) {
+  return w == 0.f && !off ? -0.f : w;
+}
 __device__ __forceinline__ bool not_finite(float x) {
   return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u;
 }
@@ -410,7 +415,6 @@ struct GenSmem {
   float v[kGenU][DP];
   float q[kGenR][DP];
   float p[kGenR][kGenU];
-  uint32_t seen[kGenR];  // in a tail: the keys that a row sees
   float alpha[kGenR], m[kGenR], l[kGenR];
   const unsigned char* row_k[kGenU];
   const unsigned char* row_v[kGenU];
@@ -532,6 +536,7 @@ __global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const Atten
       for (int j = 0; j < 4; ++j) {
         const int r = warp + 4 * j;
         float x = z[j] * p.scale_log2;
+        bool off = false;
         if (tail) {
           const int i = min(fast_div(row0 + r, p.div_g), cur.q - 1);
           bool on = pos < cur.kv || (pos < len && pos - cur.kv <= i);
@@ -541,13 +546,14 @@ __global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const Atten
                                           : att_tree_bits(par, i, 0, kGenU + lo, tree_ok) << -lo;
             on = pos < cur.kv || (bits >> lane & 1u);
           }
-          if (!on) x = -INFINITY;
-          const uint32_t bits = __ballot_sync(0xffffffffu, on);
-          if (lane == 0) sm.seen[r] = bits;
+          off = !on;
+          if (off) x = -INFINITY;
         }
         const float mn = fmaxf(m[j], warp_max(x));
         const float ms = mn == -INFINITY ? 0.f : mn;
-        const float a = exp2f(m[j] - ms), pr = exp2f(x - ms);
+        const float a = exp2f(m[j] - ms);
+        float pr = exp2f(x - ms);
+        if (tail) pr = att_mark_seen(pr, off);
         m[j] = mn;
         l[j] = l[j] * a + pr;
         sm.p[r][lane] = pr;
@@ -582,13 +588,13 @@ __global__ void __launch_bounds__(kGenThreads) attend_general_kernel(const Atten
           }
         }
       } else {
-        // keys that only some rows see leave the others as they are, whatever
-        // their values hold
+        // keys that only some rows see leave the others (weight +0) as they
+        // are, whatever their values hold
         for (int key = 0; key < kGenU; ++key)
 #pragma unroll
           for (int r = 0; r < kRows; ++r) {
             const float pr = sm.p[rg + r][key];
-            const bool on = sm.seen[rg + r] >> key & 1u;
+            const bool on = __float_as_uint(pr) != 0;
 #pragma unroll
             for (int c = 0; c < kCols; ++c) {
               float& o = acc[r * kCols + c];

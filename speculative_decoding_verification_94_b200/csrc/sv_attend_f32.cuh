@@ -189,16 +189,15 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_f32_kernel(const Attend
       const int pos0 = t * kF32U + warp * kF32Keys;
       const bool tail = pos0 + kF32Keys > kv;
       float alpha[kRL];
-      uint32_t seen[kRL];  // in a tail: the keys that this lane's rows see
       bool grew = false;
 #pragma unroll
       for (int i = 0; i < kRL; ++i) {
         x[i] *= p.scale_log2;
-        seen[i] = 0;
+        bool off = false;
         if (tail) {
           const int tok = min(fast_div(row0 + quarter * kRL + i, p.div_g), cur.q - 1);
-          seen[i] = att_tail_bits<kF32Keys>(par, tok, pos0, kv, tree_ok);
-          if (!(seen[i] >> key & 1u)) x[i] = -INFINITY;
+          off = !(att_tail_bits<kF32Keys>(par, tok, pos0, kv, tree_ok) >> key & 1u);
+          if (off) x[i] = -INFINITY;
         }
         float top = x[i];
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
@@ -210,6 +209,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_f32_kernel(const Attend
         grew |= mn != m[i];
         m[i] = mn;
         x[i] = exp2f(x[i] - ms);
+        if (tail) x[i] = att_mark_seen(x[i], off);
         l[i] = l[i] * alpha[i] + x[i];
         s_p[(quarter * kRL + i) * kF32Keys + key] = make_float2(x[i], x[i]);
       }
@@ -246,13 +246,12 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_f32_kernel(const Attend
               acc[r][e] = f2_fma(p1, v1[e], acc[r][e]);
             }
           } else {
-            // keys that only some rows see leave the others as they are,
-            // whatever their values hold
-            const uint32_t on = __shfl_sync(0xffffffffu, seen[r % kRL], r / kRL) >> 2 * a;
+            // keys that only some rows see leave the others (weight +0) as
+            // they are, whatever their values hold
 #pragma unroll
             for (int e = 0; e < kV2; ++e) {
-              if (on & 1u) acc[r][e] = f2_fma(p0, v0[e], acc[r][e]);
-              if (on & 2u) acc[r][e] = f2_fma(p1, v1[e], acc[r][e]);
+              if (p0 != 0) acc[r][e] = f2_fma(p0, v0[e], acc[r][e]);
+              if (p1 != 0) acc[r][e] = f2_fma(p1, v1[e], acc[r][e]);
             }
           }
         }
