@@ -24,11 +24,13 @@
 // it was 64 or 128 wide, so a tile's 16 take 0.8 us (24 with 128 rows: 1.2 us),
 // and a softmax of 128 rows 0.9 us without the rests.  With the products and the
 // softmax taken out, the copies alone needed 109 us for 130,000 keys of 8 heads
-// (40 rows).  What the rests cost: 69.7 -> 70.6 us with 28 rows (32 requests of
-// 700 to 9000 keys), 105.7 -> 112.3 us with 40 (130,000 keys), 49.4 -> 61.5 us
-// with 256 (8 requests of 2000 to 8000 keys; 9 us of it in the softmax, 3 in the
-// products).  In second products for all numbers of rows: 74, 117 and 61.5 us.
-// What was slower too: S in halves of 64 keys (32 instructions a tile).
+// (40 rows).  What the rests cost: 67.3 -> 68.3 us with 28 rows (32 requests of
+// 700 to 9000 keys), 100 -> 107 us with 40 (130,000 keys), 49 -> 59 us with 256
+// (8 requests of 2000 to 8000 keys), 191 -> 235 us with 128 (64 requests), there
+// mostly in the softmax.  What was slower: second products for all numbers of
+// rows (74 and 117 us with 28 and 40); S in halves of 64 keys (32 instructions a
+// tile); with 128 rows, half of a tile's second product under the other half's
+// softmax (244 us).
 //
 // Roles.  Two warps issue the copies (keys, values), one the products, as
 // their operands arrive, one fills the rows behind a request's own.  Two warp
@@ -138,6 +140,12 @@ __device__ __forceinline__ void tc_st(uint32_t a, const uint32_t (&r)[16]) {
                "%8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
                "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
                "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void tc_st(uint32_t a, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(
+                   r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(a)
                : "memory");
 }
 __device__ __forceinline__ void tc_ld(uint32_t a, uint32_t (&r)[32]) {
@@ -512,7 +520,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         tc_fence_after();
         // S is read twice, 32 columns at a time, for the maximum and for the
-        // weights: tensor memory is near, registers are not plenty.
+        // weights (but for the last two chunks, which are still there: the
+        // weights begin with them); registers are not plenty, which is also why
+        // 128 rows store theirs 16 keys at a time (64 requests x 16 tokens x 8
+        // heads: 259 us in order and with 32, 241, 235).
         // The chunks of this copy, then those of its partner, whose weights'
         // rests go to this copy's lanes.
         constexpr int kOwn = kKeys / 32, kChunks = kCopies > 1 ? 2 * kOwn : kOwn;
@@ -535,10 +546,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint32_t x[2][32];
         float top = -INFINITY;
         tc_ld(s_at + chunk(0) * 32, x[0]);
+        if (kSeen > 2) tc_ld(s_at + chunk(1) * 32, x[1]);
 #pragma unroll
         for (int c = 0; c < kSeen; ++c) {
           tc_wait_ld(x[c & 1]);
-          if (c + 1 < kSeen) tc_ld(s_at + chunk(c + 1) * 32, x[(c + 1) & 1]);
+          if (kSeen == 2 && c == 0) tc_ld(s_at + chunk(1) * 32, x[1]);
+          if (kSeen > 2 && c == 2) tc_ld(s_at + chunk(3) * 32, x[1]);
           hide(c, x[c & 1]);
           float t2[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -546,8 +559,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             t2[(e >> 1) & 3] = max3(t2[(e >> 1) & 3], __uint_as_float(x[c & 1][e]),
                                     __uint_as_float(x[c & 1][e + 1]));
           top = fmaxf(fmaxf(t2[0], t2[1]), fmaxf(t2[2], t2[3]));
+          if (kSeen > 2 && c == 0) tc_ld(s_at + chunk(2) * 32, x[0]);
         }
-        if (kSeen > 2) tc_ld(s_at + chunk(0) * 32, x[0]);  // two are still there
         if constexpr (kSeen < kChunks) {
           // the partner's maximum, from shared memory; a place is written again
           // two tiles on, when everyone has passed the next one's barrier
@@ -592,15 +605,37 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // P over S: bf16 pairs in the first half of their keys' columns; the
         // rests in the second half, or in the partner's lanes
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          if (kSeen > 2) {
-            tc_wait_ld(x[c & 1]);
-            if (c + 1 < kChunks) tc_ld(s_at + chunk(c + 1) * 32, x[(c + 1) & 1]);
-            hide(c, x[c & 1]);
-          } else if (c >= kSeen) {
+        for (int i = 0; i < kChunks; ++i) {
+          const int c = (i + kSeen - 2) % kChunks;  // the last two looked at are still there
+          if (i >= 2) {
             tc_wait_ld(x[c & 1]);
             hide(c, x[c & 1]);
           }
+          if constexpr (kCopies == 1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t y[8], rest[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float a, b;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c & 1][16 * h + 2 * e]),
+                                         __uint_as_float(x[c & 1][16 * h + 2 * e + 1])),
+                                 cc, mm),
+                          a, b);
+                a = pow2(a);
+                b = pow2(b);
+                sum[e & 1] = f2_add(sum[e & 1], f2_pack(a, b));
+                y[e] = pack_bf16(a, b);
+                float ra, rb;
+                f2_unpack(f2_fma(f2_pack(bf16_lo(y[e]), bf16_hi(y[e])), f2_pack(-1.f, -1.f),
+                                 f2_pack(a, b)),
+                          ra, rb);
+                rest[e] = pack_bf16(ra, rb);
+              }
+              tc_st(s_at + chunk(c) * 32 + 8 * h, y);
+              tc_st(s_at + chunk(c) * 32 + 16 + 8 * h, rest);
+            }
+          } else {
           uint32_t y[16], rest[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -613,7 +648,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             b = pow2(b);
             if (c < kOwn) sum[e & 1] = f2_add(sum[e & 1], f2_pack(a, b));
             y[e] = pack_bf16(a, b);
-            if (kCopies == 1 || c >= kOwn) {
+            if (c >= kOwn) {
               float ra, rb;
               f2_unpack(f2_fma(f2_pack(bf16_lo(y[e]), bf16_hi(y[e])), f2_pack(-1.f, -1.f),
                                f2_pack(a, b)),
@@ -622,8 +657,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
           tc_st(s_at + chunk(c) * 32, c < kOwn ? y : rest);
-          if (kCopies == 1) tc_st(s_at + chunk(c) * 32 + 16, rest);
-          if (kSeen == 2 && c + 2 < kChunks) tc_ld(s_at + chunk(c + 2) * 32, x[c & 1]);
+          }
+          if (i + 2 < kChunks) tc_ld(s_at + chunk((c + 2) % kChunks) * 32, x[c & 1]);
         }
         if constexpr (kCopies > 2) {  // the other copies' keys
           const uint32_t zero[16] = {};
