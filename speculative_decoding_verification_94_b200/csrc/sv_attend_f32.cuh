@@ -1,10 +1,10 @@
 // sv_attend_f32.cuh -- fp32 attention of head sizes up to 128 (D is 64 or 128, the
 // columns past the head size are zeros), up to 8 rows.
 //
-// A key costs 4 D rows operations against 8 D bytes: up to about 8 rows the
-// read of the cache is the bound (32 requests of 4000 keys, 8 key heads, 4
-// rows: 1.06 GB in 200 us, 5.3 TB/s), beyond it the fp32 pipe.  The frame is that of
-// the bf16 kernel of few rows: four warps, each with its own ring of 8-key
+// A key costs 4 D rows operations against 8 D bytes: up to 4 rows the read of
+// the cache is the bound (32 requests of 4000 keys, 8 key heads, 4 rows: 1.05 GB
+// in 204 us, 5.1 TB/s), then the fp32 pipe (8 rows: 338 us).  The frame is that
+// of the bf16 kernel of few rows: four warps, each with its own ring of 8-key
 // steps, its own softmax and output.  Scores: four lanes share a key, each
 // takes every fourth 16 bytes of the row; their sums are exchanged so that
 // each of the four ends with a quarter of the rows.  Outputs: a lane holds

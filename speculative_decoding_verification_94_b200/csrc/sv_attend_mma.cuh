@@ -20,9 +20,11 @@
 // output's error grows from 0.0017 (its own rounding) to 0.0021 of its size.
 //
 // Measured: 256 requests of 100 to 4000 tokens, 8 key heads, 4 rows: 2.19 GB
-// in 332 us, 6.6 TB/s.  At 16 rows and 32 requests of 700 to 9000 tokens this
-// kernel and the tensor-memory one both take 65 us, at 28 rows 106 against
-// 70 us; with 256 requests of 100 to 300 tokens 53 against 82 us at 16 rows.
+// in 331 to 339 us under ncu, 6.5 to 6.6 TB/s (of reads alone; a copy of as many
+// bytes read and written runs at 6.55), 376 us a call among others.  At 16 rows
+// and 32 requests of 700 to 9000 tokens this kernel and the tensor-memory one
+// both take 65 us, at 28 rows 106 against 68 us; with 256 requests of 100 to 300
+// tokens 53 against 82 us at 16 rows.
 #pragma once
 
 #include "sv_attend.cuh"
@@ -30,7 +32,7 @@
 namespace sv {
 
 // What a segment costs beside its tiles, in tiles (256 requests of 100 to 4000
-// tokens: 358 us with 0, 338 with 1, 332 with 2 and with 4).
+// tokens, calls back to back: 358 us with 0, 338 with 1, 332 with 2 and with 4).
 constexpr int kMmaOv = 2;
 constexpr int kMmaThreads = 128, kMmaWarps = 4, kMmaKeys = 16, kMmaU = kMmaWarps * kMmaKeys;
 

@@ -3,9 +3,9 @@
 // zeros).
 //
 // From 16 rows on the fp32 pipe is the bound by far (32 requests of 4000 keys,
-// 16 rows: 680 us against 163 us for the read; this kernel 280).  Here the products go
-// through the tensor cores in tf32, which has 11 bits: each operand is the
-// sum of two tf32 numbers, x = h + l, and a product is three, h h' + h l' + l h'.
+// 16 rows: 680 us against 160 us for the read; this kernel 291).  Here the
+// products go through the tensor cores in tf32, which has 11 bits: each operand
+// is the sum of two tf32 numbers, x = h + l, and a product is three, h h' + h l' + l h'.
 // Weights and q round h to nearest (|l| <= 2^-11 |x|), keys and values cut
 // it off (|l| <= 2^-10 |x|, one instruction, and nothing overflows); l rounds
 // to nearest.  What that leaves out of a product is at most 2^-21 + 2^-21 +
@@ -69,7 +69,7 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 // A B alone.  The tensor core cuts its sums off, which adds up over thousands
-// of steps (60,000 keys: an error of 1.7e-5 of the output, 1.5e-6 without): a
+// of steps (60,000 keys: an error of 1.7e-5 of the output, 7.5e-7 without): a
 // step's product, and every four of a score, are added by fp32 additions.
 __device__ __forceinline__ void mma_tf32_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                                uint32_t b1) {

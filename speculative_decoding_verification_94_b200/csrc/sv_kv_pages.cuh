@@ -39,8 +39,9 @@ inline size_t plan_smem(int B) { return (size_t)B * 6 * sizeof(int32_t); }
 
 // Threads of the block: one for each request or for every four slots, since
 // the time of a small plan is that of its barriers and of three loads one after
-// another (B = 32: 8.2 us with 128 threads, 10.2 us with 1024); all of them
-// for steps with prompts, which move thousands of pages.
+// another (B = 32, events around one call: 8.2 us with 128 threads, 10.2 us with
+// 1024; 5.8 us a call among others); all of them for steps with prompts, which
+// move thousands of pages.
 inline int plan_threads(int B, long long slots) {
   if (slots > kPlanInlineSlots) return kPlanMaxThreads;
   const long long want = B > slots / 4 ? B : slots / 4;
