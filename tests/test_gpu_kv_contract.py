@@ -311,3 +311,50 @@ def test_attend_strides_that_are_never_taken_change_nothing(n, hq, dtype):
     for c, was in zip((s["kc"], s["vc"]), old):
         was[0, 4], was[0, 5] = was[0, 5].clone(), was[0, 8].clone()
         assert torch.equal(c, was)
+
+
+FIRST_IN_A_GRAPH = """
+import torch
+from speculative_decoding_verification_94_b200 import sv
+from tests.test_gpu_kv import DEV, i32, scenario, status
+sv.lib()
+cases = []
+for n, hq, dtype in ((1, 4, "bf16"), (8, 8, "bf16"), (20, 16, "bf16"), (2, 4, "f32"), (8, 8, "f32")):
+    s = scenario(2, n, hq, 2, 64, 16, [30, 70], dtype, seed=n)
+    cases.append((s, i32(s["table"]), i32(s["kv_len"])))
+state = dict(kv=i32([3, 0]), table=i32([[0, -1], [-1, -1]]), pages=i32([1, 0]),
+             free=i32([1, 2, 3, -1]), count=i32([3]), new=i32([2, 5]), nodes=i32([[0, 2], [0, 1]]),
+             acc=i32([1, 1]), kc=torch.randn(4, 16, 1, 8, device=DEV), st=status())
+state["vc"] = state["kc"].clone()
+x = torch.randn(2, 5, 1, 8, device=DEV)
+before = {k: v.clone() for k, v in state.items()}
+def run():
+    outs = [sv.sv_kv_attend(s["q"], s["kc"], s["vc"], t, l, device_status=state["st"])
+            for s, t, l in cases]
+    p = sv.sv_kv_plan(state["kv"], state["table"], state["pages"], state["free"], state["count"],
+                      state["new"], 5, 16, device_status=state["st"])
+    sv.sv_kv_append(x, x, p["slot_map"], state["kc"], state["vc"], device_status=state["st"])
+    sv.sv_kv_commit(state["kc"], state["vc"], state["table"], p["kv_len"], state["nodes"],
+                    state["acc"], q_len=p["q_len"], device_status=state["st"])
+    return [o[k] for o in outs for k in ("out", "lse")] + list(p.values())
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = run()
+g.replay()
+torch.cuda.synchronize()
+after = {k: v.clone() for k, v in state.items()}
+for k, v in before.items():
+    state[k].copy_(v)
+want = run()
+assert int(state["st"].item()) == int(after["st"].item())
+for a, b in zip(got + list(after.values()), want + list(state.values())):
+    assert torch.equal(a, b)
+print("graph ok")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_A_GRAPH], cwd=ROOT, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "graph ok" in r.stdout, r.stderr[-2000:]
