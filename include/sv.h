@@ -527,6 +527,8 @@ SV_API sv_status sv_kv_attend(const sv_kv_cache* cache, const void* q, int64_t b
  *   accepted_nodes [B, width] and accepted_len [B] as sv_verify_tree_* give
  *   them (width = max_depth + 1 <= 1024; the path ascends from node 0; entries
  *   past the path are ignored; accepted_len -1 or 0 moves nothing).
+ *   Every request with accepted_len above 0 must have been in the step with all
+ *   its nodes; where the plan may have left some out, sv_kv_commit_ragged.
  *   A path that does not ascend from 0 sets SV_DEV_BAD_TREE, a position
  *   outside the table or accepted_len >= width SV_DEV_BAD_LEN, a bad page
  *   SV_DEV_BAD_INDEX; such a request's cache is left as it is.
